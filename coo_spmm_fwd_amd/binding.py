@@ -23,7 +23,8 @@ EXPORTED = ["sparse_layer_create", "sparse_layer_destroy", "spmm_fwd", "spmm_fwd
             "restructure", "sparse_layer_nnz", "sparse_layer_shape", "sparse_layer_export",
             "sparse_layer_export_index", "sparse_layer_values", "sparse_layer_set_values", "sparse_layer_time_next",
             "sparse_layer_last_error", "restructure_async", "sparse_layer_sync", "spmm_batch_minor", "spmm_fwd_bm",
-            "spmm_bwd_bm"]
+            "spmm_bwd_bm", "embed_fwd", "embed_bwd", "embed_bwd_workspace", "linear_ce_fwd", "linear_ce_bwd",
+            "linear_ce_workspace", "grad_norm", "grad_clip", "grad_clip_workspace"]
 
 
 class CspError(RuntimeError):
@@ -97,6 +98,28 @@ def load(path: str = LIB_PATH):
     L.sparse_layer_time_next.argtypes = [c_void_p, c_void_p, c_void_p]
     L.sparse_layer_last_error.restype = c_char_p
     L.sparse_layer_last_error.argtypes = []
+    L.embed_fwd.restype = c_int
+    L.embed_fwd.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_float, c_void_p, c_void_p]
+    L.embed_bwd.restype = c_int
+    L.embed_bwd.argtypes = [c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_float, c_void_p, c_void_p, c_int64,
+                            c_void_p]
+    L.embed_bwd_workspace.restype = c_int64
+    L.embed_bwd_workspace.argtypes = [c_int64, c_int64, c_int64, c_int]
+    L.linear_ce_fwd.restype = c_int
+    L.linear_ce_fwd.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p,
+                                c_void_p, c_void_p, c_int64, c_void_p]
+    L.linear_ce_bwd.restype = c_int
+    L.linear_ce_bwd.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p,
+                                c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]
+    L.linear_ce_workspace.restype = c_int64
+    L.linear_ce_workspace.argtypes = [c_int64, c_int64, c_int64, c_int, c_int32]
+    L.grad_norm.restype = c_int
+    L.grad_norm.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p]
+    L.grad_clip.restype = c_int
+    L.grad_clip.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_float, c_void_p, c_void_p, c_int64,
+                            c_void_p]
+    L.grad_clip_workspace.restype = c_int64
+    L.grad_clip_workspace.argtypes = [c_int64]
     _lib = L
     return L
 
@@ -445,6 +468,178 @@ def sparse_layer_set_values(layer: int, vals, stream=None):
     nnz = sparse_layer_nnz(layer)
     vp = None if vals is None else _dev(vals, "vals", _torch_dtype(dt), (nnz,))
     _check(load().sparse_layer_set_values(c_void_p(layer), vp, _stream(stream)))
+
+
+# ------------------------------------------------------------ token operators
+def _new(shape, dtype, device, stream):
+    """A new tensor for work on `stream`: allocated in that stream's pool, so that memory freed on
+    another stream is not handed to it early, and held for the current stream too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    here = torch.cuda.current_stream(device)
+    if s == here:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def _work(nbytes: int, device, stream):
+    if nbytes < 0:
+        raise CspError(-1, sparse_layer_last_error())
+    return _new(nbytes, _torch().uint8, device, stream)
+
+
+def _device(*tensors):
+    """The one device of all tensors, which has to be the current one (its stream is used)."""
+    torch = _torch()
+    d = tensors[0].device
+    if any(t.device != d for t in tensors):
+        raise ValueError("tensors are on different devices")
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {d}, which is not the current device")
+    return d
+
+
+def _matrix(t, name, dtype=None):
+    """Pointer and shape of a contiguous fp32 or bf16 GPU matrix."""
+    p = _dev(t, name, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    return p, int(t.shape[0]), int(t.shape[1])
+
+
+def embed_fwd(E, ids, scale: float = 1.0, Y=None, stream=None):
+    """Y[n, :] = scale * E[ids[n], :]; ids int64 [N], a zero row for an id outside [0, V)."""
+    torch = _torch()
+    ep, V, D = _matrix(E, "E")
+    dt = _dtype_code(E)
+    N = int(ids.numel())
+    ip = _dev(ids, "ids", torch.int64, (N,))
+    if Y is None:
+        Y = _new((N, D), E.dtype, E.device, stream)
+    yp = _dev(Y, "Y", E.dtype, (N, D))
+    _device(E, ids, Y)
+    _check(load().embed_fwd(ep, ip, N, V, D, dt, float(scale), yp, _stream(stream)))
+    return Y
+
+
+def embed_bwd(dY, ids, V: int, scale: float = 1.0, dE=None, stream=None):
+    """dE[v, :] = scale * sum over n with ids[n] = v of dY[n, :], as [V, D] (zero rows where no id is v)."""
+    torch = _torch()
+    gp, N, D = _matrix(dY, "dY")
+    dt = _dtype_code(dY)
+    V = int(V)
+    ip = _dev(ids, "ids", torch.int64, (N,))
+    L = load()
+    w = _work(L.embed_bwd_workspace(N, V, D, dt), dY.device, stream)
+    if dE is None:
+        dE = _new((V, D), dY.dtype, dY.device, stream)
+    ep = _dev(dE, "dE", dY.dtype, (V, D))
+    _device(dY, ids, dE)
+    _check(L.embed_bwd(gp, ip, N, V, D, dt, float(scale), ep, c_void_p(w.data_ptr()), w.numel(), _stream(stream)))
+    return dE
+
+
+def linear_ce_fwd(X, W, targets, loss=None, lse=None, total=None, stream=None):
+    """Cross entropy of the logits X W^T against int64 targets, the logits not stored: fp32 tensors
+    loss [N], lse [N] and total = {sum, count, mean} over the targets inside [0, V)."""
+    torch = _torch()
+    xp, N, D = _matrix(X, "X")
+    wp, V, D2 = _matrix(W, "W", X.dtype)
+    if D2 != D:
+        raise ValueError(f"X is {N} x {D} but W is {V} x {D2}")
+    dt = _dtype_code(X)
+    tp = _dev(targets, "targets", torch.int64, (N,))
+    L = load()
+    w = _work(L.linear_ce_workspace(N, V, D, dt, 0), X.device, stream)
+    loss = _new((N,), torch.float32, X.device, stream) if loss is None else loss
+    lse = _new((N,), torch.float32, X.device, stream) if lse is None else lse
+    total = _new((3,), torch.float32, X.device, stream) if total is None else total
+    op, ep = _dev(loss, "loss", torch.float32, (N,)), _dev(lse, "lse", torch.float32, (N,))
+    sp = _dev(total, "total", torch.float32, (3,))
+    _device(X, W, targets, loss, lse, total)
+    _check(L.linear_ce_fwd(xp, wp, tp, N, V, D, dt, op, ep, sp, c_void_p(w.data_ptr()), w.numel(), _stream(stream)))
+    return loss, lse, total
+
+
+def linear_ce_bwd(X, W, targets, lse, dmean, total, dX=None, dW=None, stream=None):
+    """Gradients (dX, dW) of dmean * mean loss; lse and total from linear_ce_fwd, dmean fp32 [1]."""
+    torch = _torch()
+    xp, N, D = _matrix(X, "X")
+    wp, V, D2 = _matrix(W, "W", X.dtype)
+    if D2 != D:
+        raise ValueError(f"X is {N} x {D} but W is {V} x {D2}")
+    dt = _dtype_code(X)
+    tp = _dev(targets, "targets", torch.int64, (N,))
+    ep = _dev(lse, "lse", torch.float32, (N,))
+    gp, sp = _dev(dmean, "dmean", torch.float32, (1,)), _dev(total, "total", torch.float32, (3,))
+    L = load()
+    w = _work(L.linear_ce_workspace(N, V, D, dt, 1), X.device, stream)
+    dX = _new((N, D), X.dtype, X.device, stream) if dX is None else dX
+    dW = _new((V, D), X.dtype, X.device, stream) if dW is None else dW
+    dxp, dwp = _dev(dX, "dX", X.dtype, (N, D)), _dev(dW, "dW", X.dtype, (V, D))
+    _device(X, W, targets, lse, dmean, total, dX, dW)
+    _check(L.linear_ce_bwd(xp, wp, tp, N, V, D, dt, ep, gp, sp, dxp, dwp, c_void_p(w.data_ptr()), w.numel(),
+                           _stream(stream)))
+    return dX, dW
+
+
+def _tensor_list(ts, name, like=None):
+    """Host arrays of pointers, element counts and dtype codes of a list of GPU tensors."""
+    torch = _torch()
+    codes = {torch.float32: CSP_F32, torch.bfloat16: CSP_BF16}
+    n = len(ts)
+    for t in ts:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be GPU tensors")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dtype not in codes:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+    if like is not None:
+        if len(like) != n:
+            raise ValueError(f"{n} {name} for {len(like)} gradients")
+        for t, g in zip(ts, like):
+            if t.dtype != g.dtype or t.numel() != g.numel():
+                raise ValueError(f"{name} must have the gradients' types and sizes")
+    if n:
+        _device(*ts)
+    return ((c_void_p * n)(*[t.data_ptr() for t in ts]), (c_int64 * n)(*[t.numel() for t in ts]),
+            (c_int32 * n)(*[codes[t.dtype] for t in ts]))
+
+
+def _norm_out(grads, norm, stream):
+    torch = _torch()
+    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    L = load()
+    w = _work(L.grad_clip_workspace(len(grads)), dev, stream)
+    norm = _new((1,), torch.float32, dev, stream) if norm is None else norm
+    return L, w, norm, _dev(norm, "norm", torch.float32, (1,))
+
+
+def grad_norm(grads, norm=None, stream=None):
+    """The 2-norm of all elements of a list of fp32 and bf16 tensors, as an fp32 tensor [1]."""
+    grads = list(grads)
+    gp, nn, dt = _tensor_list(grads, "grads")
+    L, w, norm, np_ = _norm_out(grads, norm, stream)
+    _check(L.grad_norm(gp, nn, dt, len(grads), np_, c_void_p(w.data_ptr()), w.numel(), _stream(stream)))
+    return norm
+
+
+def grad_clip(grads, max_norm: float, outs=None, norm=None, stream=None):
+    """Multiply every tensor by min(1, max_norm / (norm + 1e-6)), in place or into `outs`; returns
+    the norm before clipping, as an fp32 tensor [1] (nothing is read back to the host)."""
+    grads = list(grads)
+    gp, nn, dt = _tensor_list(grads, "grads")
+    op = gp if outs is None else _tensor_list(list(outs), "outs", grads)[0]
+    L, w, norm, np_ = _norm_out(grads, norm, stream)
+    _check(L.grad_clip(gp, op, nn, dt, len(grads), float(max_norm), np_, c_void_p(w.data_ptr()), w.numel(),
+                       _stream(stream)))
+    return norm
 
 
 class LayerOwner:

@@ -373,6 +373,86 @@ csp_status sparse_layer_set_values(sparse_layer_t layer, const void *vals, void 
  */
 csp_status sparse_layer_time_next(sparse_layer_t layer, void *ev_before, void *ev_after);
 
+/*
+ * Token operators: the two ends of a language model around the sparse layers
+ * (the page reports end-to-end GPT-2 training, Abstract, and leaves these
+ * steps to the surrounding model).  They need no layer.  Token ids and targets
+ * are int64 device arrays; an id or target outside [0, V) takes no part.
+ * dtype is the type of the named matrices; sums are fp32, and each output is
+ * rounded once.  A call that needs scratch memory takes a device workspace of
+ * the caller (16-byte aligned, at least the bytes its _workspace function
+ * says, contents undefined before and after).  All are asynchronous on
+ * "stream", allocate nothing and may be captured in a HIP graph.  No float
+ * result depends on the order of atomics: the same inputs give the same bits.
+ * Limits: N, V, D < 2^31; N = 0 is valid.  The _workspace functions return -1
+ * for arguments that the call would refuse.
+ */
+
+/*
+ * embed_fwd -- embedding lookup: Y[n, :] = scale * E[ids[n], :], E [V, D],
+ * Y [N, D]; a zero row for an id that takes no part.
+ */
+csp_status embed_fwd(const void *E, const int64_t *ids, int64_t N, int64_t V, int64_t D, csp_dtype dtype, float scale,
+                     void *Y, void *stream);
+
+/*
+ * embed_bwd -- its gradient: dE[v, :] = scale * sum over n with ids[n] = v of
+ * dY[n, :], every row of dE [V, D] written (zero where no id names it).
+ */
+csp_status embed_bwd(const void *dY, const int64_t *ids, int64_t N, int64_t V, int64_t D, csp_dtype dtype, float scale,
+                     void *dE, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t embed_bwd_workspace(int64_t N, int64_t V, int64_t D, csp_dtype dtype);
+
+/*
+ * linear_ce_fwd -- softmax cross entropy of the logits z = X W^T, X [N, D],
+ * W [V, D], against targets [N], without storing the logits:
+ *     lse[n]  = log sum_v exp z[n, v]
+ *     loss[n] = lse[n] - z[n, targets[n]]
+ *     total   = {sum of loss, count, sum / max(count, 1)}, over the tokens
+ *               that take part
+ * loss, lse and total are fp32.  A token that takes no part has loss and lse
+ * 0, whatever its row of X holds.
+ */
+csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
+                         csp_dtype dtype, float *loss, float *lse, float *total, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/*
+ * linear_ce_bwd -- the gradient of dmean[0] * total[2]:
+ *     G[n, v] = (exp(z[n, v] - lse[n]) - [v = targets[n]]) * dmean / count
+ *     dX = G W,   dW = G^T X
+ * with lse and total as linear_ce_fwd left them and dmean one fp32 on the
+ * device.  The logits are recomputed a piece of the vocabulary at a time.
+ * Rows of dX of tokens that take no part are 0 and such tokens add nothing to
+ * dW.  dX and dW have the dtype of X and W.
+ */
+csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
+                         csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX, void *dW,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+/* backward: 0 for linear_ce_fwd, 1 for linear_ce_bwd. */
+int64_t linear_ce_workspace(int64_t N, int64_t V, int64_t D, csp_dtype dtype, int32_t backward);
+
+/*
+ * grad_norm -- the 2-norm of all elements of "count" tensors together, one
+ * fp32 on the device.  grads, numel and dtypes are host arrays: device
+ * pointers (aligned to their elements), element counts and csp_dtypes.
+ * Squares are added in fp64.
+ */
+csp_status grad_norm(const void *const *grads, const int64_t *numel, const int32_t *dtypes, int64_t count, float *norm,
+                     void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * grad_clip -- that norm, and outs[i] = grads[i] * min(1, max_norm / (norm +
+ * 1e-6)).  outs[i] is grads[i] (in place) or a tensor of the same size and
+ * type that overlaps none of the others.  A NaN norm makes every output NaN.
+ * max_norm >= 0.
+ */
+csp_status grad_clip(const void *const *grads, void *const *outs, const int64_t *numel, const int32_t *dtypes,
+                     int64_t count, float max_norm, float *norm, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+/* Workspace of grad_norm and grad_clip. */
+int64_t grad_clip_workspace(int64_t count);
+
 /* Text of the calling thread's last error ("" if none). */
 const char *sparse_layer_last_error(void);
 

@@ -9,24 +9,62 @@
 //
 // A token whose target is outside [0, V) takes no part: loss, lse and its row
 // of dX are 0 and it adds nothing to dW, whatever its row of X holds.  The
-// tokens that take part are listed first (k_ce_rows); every product runs over
-// that list alone, so masked tokens cost nothing.  The logits are never
-// stored: the forward keeps a maximum and a sum for each (vocabulary tile,
-// token); the backward recomputes the logits, a piece of the vocabulary at a
-// time, from the saved lse.
-#include "common.h"
-#include "device_util.h"
+// tokens that take part are listed first (k_ce_rows) and their rows of X
+// gathered (k_ce_gather); every product runs over that list alone, so masked
+// tokens cost nothing.  The logits are never stored: the forward keeps a
+// maximum and a sum for each (vocabulary tile, token); the backward recomputes
+// the logits, a piece of the vocabulary at a time, from the saved lse, and
+// keeps P = exp(z - lse) - [v = t] of that piece only.
+//
+// All three products run on the tile product of mfma_tile.h, each with the
+// dimension that is contiguous in its output as m, so that a lane holds 4
+// neighbours of an output row:
+//   logits  m = vocabulary, n = token,      k = width       (W and X by rows)
+//   dX      m = width,      n = token,      k = vocabulary  (W by depth, P by rows)
+//   dW      m = width,      n = vocabulary, k = token       (X and P by depth)
+// In bf16, P is rounded to bf16 to enter the products: its error, 2^-9 of each
+// term at most, is that of the rounding of the outputs, and the scale dmean /
+// count is applied to the fp32 sums after it.  In fp32, X, W and P are split
+// into three bf16 planes (mfma_tile.h).
+#include "mfma_tile.h"
 
 namespace csp {
 namespace {
 
-constexpr int kTile = 64;   // tokens and vocabulary rows (or columns) of a tile
-constexpr int kStep = 16;   // depth of a staged slice
 constexpr int kCeThreads = 256;
+constexpr int kBM = 256;       // vocabulary rows (or columns of X) of a tile
+constexpr int64_t kPad = 256;  // token and vocabulary strides are multiples of it
+constexpr float kLog2e = 1.44269504088896340736f;
 
-// Tokens that take part, in order: rows[0 .. count).  One workgroup.
+__host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// fp32 or bf16 elements as bf16 planes.
+template <typename E> struct Split;
+template <> struct Split<BF16> {
+    static constexpr bool kMany = false;
+};
+template <> struct Split<F32> {
+    static constexpr bool kMany = true;
+};
+// The next plane of x: x rounded to bf16, x left with the rest.  An infinity or NaN goes whole into
+// the first plane; a finite value that would round to infinity is cut to the largest bf16 instead.
+__device__ __forceinline__ uint16_t take_plane(float &x)
+{
+    uint16_t p = BF16::from_f(x);
+    const bool finite = (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
+    if (finite && (p & 0x7FFFu) == 0x7F80u) p -= 1;
+    x = finite ? x - __uint_as_float((uint32_t)p << 16) : 0.0f;
+    return p;
+}
+
+// Tokens that take part, in order: rows[0 .. count) and their targets tgt; slot[n] = place in that
+// list, or -1.  Clears loss and lse (if given) of the others.  One workgroup.
 __global__ __launch_bounds__(1024) void k_ce_rows(const int64_t *__restrict__ targets, int64_t N, int64_t V,
-                                                  int32_t *__restrict__ rows, int32_t *__restrict__ count)
+                                                  int32_t *__restrict__ rows, int32_t *__restrict__ tgt,
+                                                  int32_t *__restrict__ slot, int32_t *__restrict__ count,
+                                                  float *__restrict__ loss, float *__restrict__ lse)
 {
     __shared__ uint32_t lds[17];
     uint32_t run = 0;
@@ -36,106 +74,186 @@ __global__ __launch_bounds__(1024) void k_ce_rows(const int64_t *__restrict__ ta
         const bool part = t >= 0 && t < V;
         uint32_t total;
         const uint32_t at = block_exclusive_scan(part ? 1u : 0u, lds, &total);
-        if (part) rows[run + at] = (int32_t)i;
+        if (part) {
+            rows[run + at] = (int32_t)i;
+            tgt[run + at] = (int32_t)t;
+        }
+        if (i < N) {
+            slot[i] = part ? (int32_t)(run + at) : -1;
+            if (!part && loss) loss[i] = lse[i] = 0.0f;
+        }
         run += total;
     }
     if (threadIdx.x == 0) count[0] = (int32_t)run;
 }
 
-// acc[i][j] = sum over k of A(m, k) B(n, k), thread (ty, tx) of 16 x 16 holding rows m = 4 ty + i and
-// columns n = 4 tx + j of a 64 x 64 tile.
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(FA A, FB B, int64_t K, float (&acc)[4][4])
+// dst[plane][r][0 .. ld) = planes of src row (rows ? rows[r] : r), zeros past D; with `rows`, rows
+// from count up to the next multiple of 64 are zeros (the depth of dW).  One workgroup a row.
+template <typename E>
+__global__ __launch_bounds__(kCeThreads) void k_ce_gather(const typename E::T *__restrict__ src, int64_t D,
+                                                          const int32_t *__restrict__ rows,
+                                                          const int32_t *__restrict__ count,
+                                                          uint16_t *__restrict__ dst, int64_t ld, int64_t plane)
 {
-    __shared__ float a[kStep][kTile + 4], b[kStep][kTile + 4];
-    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+    const int64_t r = blockIdx.x;
+    bool real = true;
+    if (rows) {
+        const int64_t cnt = count[0];
+        if (r >= round_up(cnt, kDepth)) return;
+        real = r < cnt;
+    }
+    const int64_t from = real ? (rows ? rows[r] : r) : 0;
+    for (int64_t c = threadIdx.x; c < ld; c += kCeThreads) {
+        if constexpr (Split<E>::kMany) {
+            float x = real && c < D ? E::load(src, from * D + c) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    for (int64_t k0 = 0; k0 < K; k0 += kStep) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = j * kCeThreads + t, r = e >> 4, k = e & 15;
-            a[k][r] = k0 + k < K ? A(r, k0 + k) : 0.0f;
-            b[k][r] = k0 + k < K ? B(r, k0 + k) : 0.0f;
+            for (int p = 0; p < kPlanes; ++p) dst[p * plane + r * ld + c] = take_plane(x);
+        } else {
+            dst[r * ld + c] = real && c < D ? src[from * D + c] : (uint16_t)0;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += a[k][4 * ty + i] * b[k][4 * tx + j];
     }
 }
 
-// z of a tile: tokens m0.. (of the list), vocabulary rows n0..
-template <typename E>
-__device__ __forceinline__ void logits_tile(const typename E::T *__restrict__ X, const typename E::T *__restrict__ W,
-                                            const int32_t *__restrict__ rows, int64_t cnt, int64_t V, int64_t D,
-                                            int64_t m0, int64_t n0, float (&acc)[4][4])
+// The place of a workgroup in a grid of mt x nt tiles (and `splits` of the depth).  Workgroups go
+// round the 8 XCDs; each XCD takes one contiguous run of tiles, walked in columns 8 tiles wide, so
+// that the tiles an XCD holds at a time share operands in its L2.
+struct TilePlace {
+    int64_t m, n, split;
+    bool ok;
+};
+__device__ __forceinline__ TilePlace tile_place(int64_t mt, int64_t nt, int64_t splits)
 {
-    tile_product([&](int r, int64_t k) { return m0 + r < cnt ? E::load(X, (int64_t)rows[m0 + r] * D + k) : 0.0f; },
-                 [&](int r, int64_t k) { return n0 + r < V ? E::load(W, (n0 + r) * D + k) : 0.0f; }, D, acc);
+    const int64_t total = mt * nt * splits, b = blockIdx.x;
+    TilePlace t{0, 0, 0, b < total};
+    if (!t.ok) return t;
+    const int64_t x = b & 7, q = total >> 3, r = total & 7;
+    int64_t id = x * q + (x < r ? x : r) + (b >> 3);
+    t.split = id / (mt * nt);
+    id -= t.split * (mt * nt);
+    const int64_t grp = id / (mt * 8), rem = id - grp * mt * 8, width = nt - grp * 8 < 8 ? nt - grp * 8 : 8;
+    t.m = rem / width;
+    t.n = grp * 8 + rem % width;
+    return t;
+}
+
+// Waves of a tile with BN tokens: 256 x 256 by 2 x 4, 256 x 128 by 4 x 2, 256 x 64 by 8 x 1.
+template <int BN> struct Waves {
+    static constexpr int kM = BN == 256 ? 2 : BN == 128 ? 4 : 8, kN = kTileWaves / kM;
+    static constexpr int kPerSimd = BN == 64 ? 4 : 2;  // two workgroups a CU where LDS holds them
+};
+
+struct Logits {
+    const uint16_t *X, *W;  // planes: listed tokens [.][ldx], vocabulary rows of the piece [.][ldw]
+    int64_t ldx, ldw, planex, planew;
+    const int32_t *tgt, *count;
+    int64_t nv, v0, npad;   // vocabulary rows of the piece, its first, token stride
+    int64_t depth;
+};
+
+// Runs the logits tile of this workgroup; false if it has none.
+template <int BN, bool kMany, typename T>
+__device__ __forceinline__ bool logits_tile(const Logits &a, T &tile, TilePlace &at, char *smem)
+{
+    at = tile_place(ceil_div(a.nv, kBM), ceil_div((int64_t)a.count[0], BN), 1);
+    if (!at.ok) return false;
+    const int64_t m0 = at.m * kBM, n0 = at.n * BN;
+    const TileOperand A{a.W + m0 * a.ldw, a.ldw, a.planew, (int32_t)(a.nv - m0 < kBM ? a.nv - m0 : kBM)};
+    const TileOperand B{a.X + n0 * a.ldx, a.ldx, a.planex, BN};
+    tile.run(A, B, a.depth, kMany, smem);
+    return true;
 }
 
 // Per (vocabulary tile, listed token): maximum and sum of exp(z - maximum); the target's logit.
-template <typename E>
-__global__ __launch_bounds__(kCeThreads) void k_ce_stats(const typename E::T *__restrict__ X,
-                                                         const typename E::T *__restrict__ W,
-                                                         const int64_t *__restrict__ targets,
-                                                         const int32_t *__restrict__ rows,
-                                                         const int32_t *__restrict__ count, int64_t N, int64_t V,
-                                                         int64_t D, float2 *__restrict__ part, float *__restrict__ zt)
+template <int BN, bool kMany>
+__global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_stats(Logits a, float2 *__restrict__ part,
+                                                                                float *__restrict__ zt)
 {
-    const int64_t cnt = count[0], m0 = (int64_t)blockIdx.y * kTile, n0 = (int64_t)blockIdx.x * kTile;
-    if (m0 >= cnt) return;
-    float z[4][4];
-    logits_tile<E>(X, W, rows, cnt, V, D, m0, n0, z);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    using T = Tile<false, false, kBM, BN, Waves<BN>::kM, Waves<BN>::kN>;
+    __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
+    T tile;
+    TilePlace at;
+    if (!logits_tile<BN, kMany>(a, tile, at, smem)) return;
+    const int l = threadIdx.x & 63, g = l >> 4, wm = T::wave_m(), wn = T::wave_n();
+    const int64_t cnt = a.count[0], vw = at.m * kBM + wm * (16 * T::FM);  // the wave's first row of the piece
+    float2 *join = (float2 *)smem;                                        // [wave row][BN]
+    const bool edge = at.m * kBM + kBM > a.nv;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 4 * ty + i;
-        const int64_t t = m < cnt ? targets[rows[m]] : -1;
-        float mx = -INFINITY, s = 0.0f;
+    for (int j = 0; j < T::FN; ++j) {
+        const int nl = (wn * T::FN + j) * 16 + (l & 15);
+        const int64_t n = at.n * BN + nl;
+        const int64_t t = n < cnt ? a.tgt[n] - a.v0 - vw - 4 * g : -1;  // relative to the lane's first row
+        float mx = -INFINITY, z = 0.0f;
+        bool hit = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t v = n0 + 4 * tx + j;
-            if (v >= V) continue;
-            if (v == t) zt[m] = z[i][j];
-            mx = fmaxf(mx, z[i][j]);
-        }
+        for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-        for (int off = 8; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+            for (int r = 0; r < 4; ++r) {
+                float x = tile.acc[i][j][r];
+                if (edge && vw + 16 * i + 4 * g + r >= a.nv) x = -INFINITY;
+                tile.acc[i][j][r] = x;
+                if (t == 16 * i + r) {
+                    z = x;
+                    hit = true;
+                }
+                mx = fmaxf(mx, x);
+            }
+        if (hit) zt[n] = z;
+        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        const float base = mx == -INFINITY ? 0.0f : mx;  // nothing of the vocabulary in this wave
+        float s = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n0 + 4 * tx + j < V) s += expf(z[i][j] - mx);
+        for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-        for (int off = 8; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
-        if (tx == 0 && m < cnt) part[(int64_t)blockIdx.x * N + m] = make_float2(mx, s);
+            for (int r = 0; r < 4; ++r) s += exp_of(tile.acc[i][j][r] - base);
+        s += __shfl_xor(s, 16, 64);
+        s += __shfl_xor(s, 32, 64);
+        if (g == 0) join[wm * BN + nl] = make_float2(mx, s);
+    }
+    __syncthreads();
+    for (int nl = threadIdx.x; nl < BN; nl += kTileThreads) {
+        const int64_t n = at.n * BN + nl;
+        if (n >= cnt) continue;
+        float mx = join[nl].x, s = 0.0f;
+        for (int w = 1; w < Waves<BN>::kM; ++w) mx = fmaxf(mx, join[w * BN + nl].x);
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        for (int w = 0; w < Waves<BN>::kM; ++w)
+            s += join[w * BN + nl].y * exp_of(join[w * BN + nl].x - base);
+        part[(a.v0 / kBM + at.m) * a.npad + n] = make_float2(mx, s);
     }
 }
 
-__global__ void k_ce_clear(int64_t N, float *__restrict__ loss, float *__restrict__ lse)
+// Joins the tiles' maxima and sums: 16 threads a token, each over every 16th tile.
+__global__ __launch_bounds__(1024) void k_ce_join(const float2 *__restrict__ part, const float *__restrict__ zt,
+                                                  const int32_t *__restrict__ rows, const int32_t *__restrict__ count,
+                                                  int64_t npad, int64_t tiles, float *__restrict__ loss,
+                                                  float *__restrict__ lse)
 {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < N) loss[i] = lse[i] = 0.0f;
-}
-
-__global__ void k_ce_join(const float2 *__restrict__ part, const float *__restrict__ zt,
-                          const int32_t *__restrict__ rows, const int32_t *__restrict__ count, int64_t N, int64_t tiles,
-                          float *__restrict__ loss, float *__restrict__ lse)
-{
-    const int64_t m = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (m >= count[0]) return;
+    __shared__ float2 join[16][64];
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t m = (int64_t)blockIdx.x * 64 + l, cnt = count[0];
+    if ((int64_t)blockIdx.x * 64 >= cnt) return;
     float mx = -INFINITY, s = 0.0f;
-    for (int64_t t = 0; t < tiles; ++t) mx = fmaxf(mx, part[t * N + m].x);
-    for (int64_t t = 0; t < tiles; ++t) s += part[t * N + m].y * expf(part[t * N + m].x - mx);
-    const float l = mx + logf(s);
-    lse[rows[m]] = l;
-    loss[rows[m]] = l - zt[m];
+    if (m < cnt) {
+        for (int64_t t = w; t < tiles; t += 16) {
+            const float2 p = part[t * npad + m];
+            const float up = fmaxf(mx, p.x);
+            const float base = up == -INFINITY ? 0.0f : up;
+            s = s * exp_of(mx - base) + p.y * exp_of(p.x - base);
+            mx = up;
+        }
+    }
+    join[w][l] = make_float2(mx, s);
+    __syncthreads();
+    if (w != 0 || m >= cnt) return;
+    mx = -INFINITY;
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, join[i][l].x);
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    s = 0.0f;
+    for (int i = 0; i < 16; ++i) s += join[i][l].y * exp_of(join[i][l].x - base);
+    const float r = mx + logf(s);
+    lse[rows[m]] = r;
+    loss[rows[m]] = r - zt[m];
 }
 
 __global__ __launch_bounds__(1024) void k_ce_total(const float *__restrict__ loss, const int32_t *__restrict__ count,
@@ -157,31 +275,126 @@ __global__ __launch_bounds__(1024) void k_ce_total(const float *__restrict__ los
     total[2] = (float)(r / (double)(c > 0 ? c : 1));
 }
 
-// P[m, v - v0] = exp(z - lse) - [v = t] of the listed tokens, vocabulary rows v0 .. v0 + nv.
-template <typename E>
-__global__ __launch_bounds__(kCeThreads) void k_ce_probs(const typename E::T *__restrict__ X,
-                                                         const typename E::T *__restrict__ W,
-                                                         const int64_t *__restrict__ targets,
-                                                         const float *__restrict__ lse,
-                                                         const int32_t *__restrict__ rows,
-                                                         const int32_t *__restrict__ count, int64_t V, int64_t D,
-                                                         int64_t v0, int64_t nv, float *__restrict__ P)
+// A wave's tile goes out through its own part of LDS, so that stores cover whole row segments: FN *
+// 16 output rows (n) of TM elements (m), 16 bytes of padding a row against bank conflicts.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+struct __attribute__((packed, aligned(2))) Vec16 {
+    u32x4 v;
+};
+template <int TM, int kRows, typename O>
+struct Stage {
+    static constexpr int kStride = TM * (int)sizeof(O) + 16;
+    static constexpr int kBytes = kRows * kStride;
+    static constexpr int kPer = 16 / (int)sizeof(O);          // elements of 16 bytes
+    static constexpr int kLanes = TM / kPer;                  // lanes a row
+    // Rows [0, rows) and elements [0, cols) of the staged tile to out[row * ld + element].
+    __device__ static void store(const char *mine, O *out, int64_t ld, int64_t rows, int64_t cols)
+    {
+        const int l = threadIdx.x & 63, e = (l % kLanes) * kPer;
+#pragma unroll 4
+        for (int r = l / kLanes; r < kRows; r += 64 / kLanes) {
+            if (r >= rows || e >= cols) continue;
+            const u32x4 v = *(const u32x4 *)(mine + r * kStride + (l % kLanes) * 16);
+            O *p = out + r * ld + e;
+            if (e + kPer <= cols) ((Vec16 *)p)->v = v;
+            else
+                for (int k = 0; e + k < cols; ++k) p[k] = ((const O *)(mine + r * kStride))[e + k];
+        }
+    }
+};
+
+// P of the piece (planes): P[n][v], zeros for tokens past the list and columns past the piece, so
+// that it can serve as depth up to the next multiple of 64.
+template <int BN, bool kMany>
+__global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_probs(Logits a,
+                                                                                const float *__restrict__ lse,
+                                                                                const int32_t *__restrict__ rows,
+                                                                                uint16_t *__restrict__ P, int64_t ldp,
+                                                                                int64_t planep)
 {
-    const int64_t cnt = count[0], m0 = (int64_t)blockIdx.y * kTile, n0 = (int64_t)blockIdx.x * kTile;
-    if (m0 >= cnt) return;
-    float z[4][4];
-    logits_tile<E>(X, W + v0 * D, rows, cnt, nv, D, m0, n0, z);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    using T = Tile<false, false, kBM, BN, Waves<BN>::kM, Waves<BN>::kN>;
+    using S = Stage<16 * T::FM, 16 * T::FN, uint16_t>;
+    constexpr int kLds = T::kLds > kTileWaves * S::kBytes ? T::kLds : kTileWaves * S::kBytes;
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    T tile;
+    TilePlace at;
+    if (!logits_tile<BN, kMany>(a, tile, at, smem)) return;
+    const int l = threadIdx.x & 63, g = l >> 4, wm = T::wave_m(), wn = T::wave_n();
+    const int64_t cnt = a.count[0], vw = at.m * kBM + wm * (16 * T::FM), nw = at.n * BN + wn * (16 * T::FN);
+    const bool edge = at.m * kBM + kBM > a.nv;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 4 * ty + i;
-        if (m >= cnt) continue;
-        const int64_t t = targets[rows[m]] - v0;
-        const float l = lse[rows[m]];
+    for (int j = 0; j < T::FN; ++j) {
+        const int64_t n = nw + j * 16 + (l & 15);
+        const bool on = n < cnt;
+        const int64_t t = on ? a.tgt[n] - a.v0 - vw - 4 * g : -1;
+        const float ls = on ? lse[rows[n]] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t v = n0 + 4 * tx + j;
-            if (v < nv) P[m * nv + v] = expf(z[i][j] - l) - (v == t ? 1.0f : 0.0f);
+        for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float p = exp_of(tile.acc[i][j][r] - ls) - (t == 16 * i + r ? 1.0f : 0.0f);
+                if (!on || (edge && vw + 16 * i + 4 * g + r >= a.nv)) p = 0.0f;
+                tile.acc[i][j][r] = p;
+            }
+    }
+    char *mine = smem + (threadIdx.x >> 6) * S::kBytes;
+#pragma unroll
+    for (int pl = 0; pl < (kMany ? kPlanes : 1); ++pl) {
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                uint16_t b[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float x = tile.acc[i][j][r];
+                    b[r] = kMany ? take_plane(x) : BF16::from_f(x);
+                    tile.acc[i][j][r] = x;
+                }
+                *(uint2 *)(mine + (j * 16 + (l & 15)) * S::kStride + (16 * i + 4 * g) * 2) =
+                    make_uint2((uint32_t)b[0] | (uint32_t)b[1] << 16, (uint32_t)b[2] | (uint32_t)b[3] << 16);
+            }
+        wait_lds();
+        S::store(mine, P + pl * planep + nw * ldp + vw, ldp, S::kBytes / S::kStride, 16 * T::FM);
+        wait_lds();
+    }
+}
+
+// acc[split][n][c] (+)= sum over the split's part of the piece of P[n, v] W[v, c].
+struct InputGrad {
+    const uint16_t *P, *W;
+    int64_t ldp, ldw, planep, planew;
+    const int32_t *count;
+    int64_t nv, D, splits, per;  // per: depth of a split, a multiple of 64
+    float *acc;
+    int64_t lda, plane;
+    int add;
+};
+template <int BN, bool kMany>
+__global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_dx(InputGrad a)
+{
+    using T = Tile<true, false, kBM, BN, Waves<BN>::kM, Waves<BN>::kN>;
+    __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
+    const int64_t cnt = a.count[0];
+    const TilePlace at = tile_place(ceil_div(a.D, kBM), ceil_div(cnt, BN), a.splits);
+    if (!at.ok) return;
+    const int64_t m0 = at.m * kBM, n0 = at.n * BN, k0 = at.split * a.per;
+    const int64_t depth = a.nv - k0 < a.per ? (a.nv - k0 > 0 ? a.nv - k0 : 0) : a.per;
+    const TileOperand A{a.W + k0 * a.ldw + m0, a.ldw, a.planew, (int32_t)(a.ldw - m0 < kBM ? a.ldw - m0 : kBM)};
+    const TileOperand B{a.P + n0 * a.ldp + k0, a.ldp, a.planep, BN};
+    T tile;
+    tile.run(A, B, depth, kMany, smem);
+    const int l = threadIdx.x & 63, g = l >> 4;
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) {
+        const int64_t n = n0 + (T::wave_n() * T::FN + j) * 16 + (l & 15);
+        if (n >= cnt) continue;
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            const int64_t c = m0 + (T::wave_m() * T::FM + i) * 16 + 4 * g;
+            if (c >= a.lda) continue;
+            f32x4 *p = (f32x4 *)(a.acc + at.split * a.plane + n * a.lda + c);
+            *p = a.add ? *p + tile.acc[i][j] : tile.acc[i][j];
         }
     }
 }
@@ -192,111 +405,143 @@ __device__ __forceinline__ float grad_scale(const float *dmean, const float *tot
     return dmean[0] / fmaxf(total[1], 1.0f);
 }
 
-// acc[m, c] += sum over the piece of P[m, v] W[v, c]; the first piece overwrites, the last one scales,
-// rounds and puts the rows in their place.
+// dX[n] = the splits' sums of its place in the list, scaled and rounded; zeros if it has none.
 template <typename E>
-__global__ __launch_bounds__(kCeThreads) void k_ce_dx(const float *__restrict__ P, const typename E::T *__restrict__ W,
-                                                      const int32_t *__restrict__ rows,
-                                                      const int32_t *__restrict__ count, int64_t D, int64_t v0,
-                                                      int64_t nv, float *__restrict__ acc, bool first, bool last,
-                                                      const float *__restrict__ dmean, const float *__restrict__ total,
-                                                      typename E::T *__restrict__ dX)
+__global__ __launch_bounds__(kCeThreads) void k_ce_dx_out(const float *__restrict__ acc, int64_t lda, int64_t plane,
+                                                          int64_t splits, const int32_t *__restrict__ slot, int64_t D,
+                                                          const float *__restrict__ dmean,
+                                                          const float *__restrict__ total,
+                                                          typename E::T *__restrict__ dX)
 {
-    const int64_t cnt = count[0], m0 = (int64_t)blockIdx.y * kTile, c0 = (int64_t)blockIdx.x * kTile;
-    if (m0 >= cnt) return;
-    float z[4][4];
-    tile_product([&](int r, int64_t k) { return m0 + r < cnt ? P[(m0 + r) * nv + k] : 0.0f; },
-                 [&](int r, int64_t k) { return c0 + r < D ? E::load(W, (v0 + k) * D + c0 + r) : 0.0f; }, nv, z);
+    const int64_t n = blockIdx.x, m = slot[n];
     const float g = grad_scale(dmean, total);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 4 * ty + i;
-        if (m >= cnt) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = c0 + 4 * tx + j;
-            if (c >= D) continue;
-            const float v = z[i][j] + (first ? 0.0f : acc[m * D + c]);
-            if (last) dX[(int64_t)rows[m] * D + c] = E::from_f(v * g);
-            else acc[m * D + c] = v;
+    for (int64_t c = threadIdx.x; c < D; c += kCeThreads) {
+        float s = 0.0f;
+        if (m >= 0) {
+            for (int64_t k = 0; k < splits; ++k) s += acc[k * plane + m * lda + c];
+            s *= g;
         }
+        dX[n * D + c] = E::from_f(s);
     }
 }
 
-// The rows of dX of tokens that take no part.
+struct WeightGrad {
+    const uint16_t *P, *X;
+    int64_t ldp, ldx, planep, planex;
+    const int32_t *count;
+    int64_t nv, D;
+    const float *dmean, *total;
+};
 template <typename E>
-__global__ __launch_bounds__(kCeThreads) void k_ce_dx_clear(const int64_t *__restrict__ targets, int64_t V, int64_t D,
-                                                            typename E::T *__restrict__ dX)
+__global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typename E::T *__restrict__ dW)
 {
-    const int64_t n = blockIdx.x, t = targets[n];
-    if (t >= 0 && t < V) return;
-    for (int64_t c = threadIdx.x; c < D; c += kCeThreads) dX[n * D + c] = E::from_f(0.0f);
-}
-
-template <typename E>
-__global__ __launch_bounds__(kCeThreads) void k_ce_dw(const float *__restrict__ P, const typename E::T *__restrict__ X,
-                                                      const int32_t *__restrict__ rows,
-                                                      const int32_t *__restrict__ count, int64_t D, int64_t v0,
-                                                      int64_t nv, const float *__restrict__ dmean,
-                                                      const float *__restrict__ total,
-                                                      typename E::T *__restrict__ dW)
-{
-    const int64_t cnt = count[0], n0 = (int64_t)blockIdx.y * kTile, c0 = (int64_t)blockIdx.x * kTile;
-    float z[4][4];
-    tile_product([&](int r, int64_t k) { return n0 + r < nv ? P[k * nv + n0 + r] : 0.0f; },
-                 [&](int r, int64_t k) { return c0 + r < D ? E::load(X, (int64_t)rows[k] * D + c0 + r) : 0.0f; }, cnt, z);
-    const float g = grad_scale(dmean, total);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    using T = Tile<true, true, kBM, 256, 2, 4>;
+    constexpr int kPass = sizeof(typename E::T) == 4 ? 2 : 1;  // fp32 rows leave in two passes
+    using S = Stage<16 * T::FM, 16 * T::FN / kPass, typename E::T>;
+    constexpr int kLds = T::kLds > kTileWaves * S::kBytes ? T::kLds : kTileWaves * S::kBytes;
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    const TilePlace at = tile_place(ceil_div(a.D, kBM), ceil_div(a.nv, 256), 1);
+    if (!at.ok) return;
+    const int64_t m0 = at.m * kBM, n0 = at.n * 256, cnt = a.count[0];
+    const TileOperand A{a.X + m0, a.ldx, a.planex, (int32_t)(a.ldx - m0 < kBM ? a.ldx - m0 : kBM)};
+    const TileOperand B{a.P + n0, a.ldp, a.planep, 256};
+    T tile;
+    tile.run(A, B, round_up(cnt, kDepth), Split<E>::kMany, smem);
+    const float s = grad_scale(a.dmean, a.total);
+    const int l = threadIdx.x & 63, g = l >> 4;
+    const int64_t mw = m0 + T::wave_m() * (16 * T::FM), nw = n0 + T::wave_n() * (16 * T::FN);
+    char *mine = smem + (threadIdx.x >> 6) * S::kBytes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t v = n0 + 4 * ty + i;
+    for (int pass = 0; pass < kPass; ++pass) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = c0 + 4 * tx + j;
-            if (v < nv && c < D) dW[(v0 + v) * D + c] = E::from_f(z[i][j] * g);
+        for (int jj = 0; jj < T::FN / kPass; ++jj) {
+            const int j = pass * (T::FN / kPass) + jj;
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                char *p = mine + (jj * 16 + (l & 15)) * S::kStride + (16 * i + 4 * g) * (int)sizeof(typename E::T);
+                const f32x4 v = tile.acc[i][j];
+                if constexpr (kPass == 2) {
+                    *(f32x4 *)p = f32x4{v[0] * s, v[1] * s, v[2] * s, v[3] * s};
+                } else {
+                    *(uint2 *)p = make_uint2((uint32_t)BF16::from_f(v[0] * s) | (uint32_t)BF16::from_f(v[1] * s) << 16,
+                                             (uint32_t)BF16::from_f(v[2] * s) | (uint32_t)BF16::from_f(v[3] * s) << 16);
+                }
+            }
         }
+        wait_lds();
+        const int64_t n = nw + pass * (16 * T::FN / kPass);
+        S::store(mine, dW + n * a.D + mw, a.D, a.nv - n, a.D - mw);
+        wait_lds();
     }
 }
 
-// Bytes of one piece's gradient at the logits.
-constexpr int64_t kPieceBytes = (int64_t)256 << 20;
+// Memory of a call is bounded whatever the vocabulary: pieces of it are taken so that P stays within
+// kPieceBytes, and the planes (or the padded copy) of W within kCopyBytes.
+constexpr int64_t kPieceBytes = (int64_t)512 << 20;
+constexpr int64_t kCopyBytesF32 = (int64_t)1 << 30, kCopyBytesBF16 = (int64_t)256 << 20;
 
 struct CePlan {
-    int64_t tiles, piece;
-    size_t rows, count, part, zt, P, acc, total;
+    int64_t npad, ldx, piece, tiles, splits;
+    int bn;
+    bool copy;  // W is copied, a piece at a time: planes, or rows that are no multiple of 128 bytes
+    size_t rows, tgt, slot, count, X, W, part, zt, P, acc, total;
 };
 
-CePlan ce_plan(int64_t N, int64_t V, int64_t D, bool backward)
+CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w_aligned)
 {
     CePlan p{};
     size_t at = 0;
-    auto take = [&](size_t bytes) {
+    auto take = [&](int64_t bytes) {
         const size_t r = at;
-        at += (bytes + 255) / 256 * 256;
+        at += (size_t)round_up(bytes, 1024);
         return r;
     };
-    p.tiles = ceil_div(V, kTile);
+    const int64_t planes = dtype == CSP_F32 ? kPlanes : 1;
+    p.npad = round_up(N > 0 ? N : 1, kPad);
+    p.ldx = round_up(D, kDepth);
+    p.bn = N <= 64 ? 64 : N <= 128 ? 128 : 256;
+    p.copy = dtype == CSP_F32 || D % kDepth != 0 || !w_aligned;
+    p.tiles = ceil_div(V, kBM);
+    p.piece = round_up(V, kPad);
+    auto limit = [&](int64_t bytes, int64_t row_bytes) {
+        int64_t r = bytes / row_bytes / kPad * kPad;
+        if (r < kPad) r = kPad;
+        if (r < p.piece) p.piece = r;
+    };
+    if (p.copy) limit(dtype == CSP_F32 ? kCopyBytesF32 : kCopyBytesBF16, planes * 2 * p.ldx);
+    if (backward) limit(kPieceBytes, planes * 2 * p.npad);
     p.count = take(4);
-    p.rows = take(4 * (size_t)N);
+    p.rows = take(4 * N);
+    p.tgt = take(4 * N);
+    p.slot = take(4 * N);
+    p.X = take(planes * 2 * p.npad * p.ldx);
+    if (p.copy) p.W = take(planes * 2 * p.piece * p.ldx);
     if (!backward) {
-        p.part = take(8 * (size_t)N * (size_t)p.tiles);
-        p.zt = take(4 * (size_t)N);
+        p.part = take(8 * p.npad * p.tiles);
+        p.zt = take(4 * p.npad);
     } else {
-        p.piece = N > 0 ? kPieceBytes / (4 * N) / kTile * kTile : V;
-        if (p.piece < kTile) p.piece = kTile;
-        if (p.piece > V) p.piece = V;
-        p.P = take(4 * (size_t)N * (size_t)p.piece);
-        p.acc = take(4 * (size_t)N * (size_t)D);
+        p.P = take(planes * 2 * p.npad * p.piece);
+        // the depth of dX is cut until its tiles fill the card about twice
+        const int64_t tiles = ceil_div(D, kBM) * ceil_div(p.npad, p.bn);
+        const int64_t most = ceil_div(p.piece, 8 * kDepth);
+        p.splits = ceil_div(512, tiles);
+        if (p.splits > most) p.splits = most;
+        p.acc = take(4 * p.splits * p.npad * p.ldx);
     }
     p.total = at;
     return p;
 }
 
+size_t ce_bytes(int64_t N, int64_t V, int64_t D, int dtype, bool backward)
+{
+    const size_t a = ce_plan(N, V, D, dtype, backward, true).total, b = ce_plan(N, V, D, dtype, backward, false).total;
+    return a > b ? a : b;
+}
+
 csp_status ce_args(int64_t N, int64_t V, int64_t D, int dtype)
 {
-    constexpr int64_t kLimit = 0x7FFFFFFF;
-    if (N < 0 || N >= kLimit || V < 1 || V >= kLimit || D < 1 || D >= kLimit)
+    constexpr int64_t kLimit = 0x7FFFFFFF - kPad;
+    if (N < 0 || N >= kLimit || V < 1 || V >= kLimit || D < 1 || D >= (int64_t)1 << 22)  // 2^22: 32-bit offsets in a tile
         return set_error(CSP_ERR_INVALID_ARG, "bad shape: %lld tokens, vocabulary %lld, width %lld", (long long)N,
                          (long long)V, (long long)D);
     if (dtype != CSP_F32 && dtype != CSP_BF16) return set_error(CSP_ERR_DTYPE, "unsupported dtype %d", dtype);
@@ -305,24 +550,62 @@ csp_status ce_args(int64_t N, int64_t V, int64_t D, int dtype)
 
 bool aligned(const void *p, size_t a) { return p && (uintptr_t)p % a == 0; }
 
+// What both directions begin with: the list, the gathered rows of X, and the Logits arguments of a piece.
+template <typename E>
+csp_status ce_begin(const CePlan &p, const void *X, const int64_t *targets, int64_t N, int64_t V, int64_t D,
+                    float *loss, float *lse, char *w, hipStream_t s)
+{
+    k_ce_rows<<<1, 1024, 0, s>>>(targets, N, V, (int32_t *)(w + p.rows), (int32_t *)(w + p.tgt),
+                                 (int32_t *)(w + p.slot), (int32_t *)(w + p.count), loss, lse);
+    CSP_LAUNCHED("k_ce_rows");
+    if (N == 0) return CSP_OK;
+    k_ce_gather<E><<<(unsigned)round_up(N, kDepth), kCeThreads, 0, s>>>(
+        (const typename E::T *)X, D, (const int32_t *)(w + p.rows), (const int32_t *)(w + p.count),
+        (uint16_t *)(w + p.X), p.ldx, p.npad * p.ldx);
+    CSP_LAUNCHED("k_ce_gather");
+    return CSP_OK;
+}
+
+template <typename E>
+csp_status ce_piece(const CePlan &p, const void *W, int64_t V, int64_t D, int64_t v0, char *w, Logits *a, hipStream_t s)
+{
+    using T = typename E::T;
+    const int64_t nv = V - v0 < p.piece ? V - v0 : p.piece;
+    *a = Logits{(const uint16_t *)(w + p.X), (const uint16_t *)((const T *)W + v0 * D), p.ldx, D, p.npad * p.ldx, 0,
+                (const int32_t *)(w + p.tgt), (const int32_t *)(w + p.count), nv, v0, p.npad, p.ldx};
+    if (!p.copy) return CSP_OK;
+    a->W = (const uint16_t *)(w + p.W);
+    a->ldw = p.ldx;
+    a->planew = p.piece * p.ldx;
+    k_ce_gather<E><<<(unsigned)nv, kCeThreads, 0, s>>>((const T *)W + v0 * D, D, nullptr, nullptr,
+                                                       (uint16_t *)(w + p.W), p.ldx, a->planew);
+    CSP_LAUNCHED("k_ce_gather");
+    return CSP_OK;
+}
+
 template <typename E>
 csp_status fwd_impl(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D, float *loss,
                     float *lse, float *total, char *w, hipStream_t s)
 {
-    using T = typename E::T;
-    const CePlan p = ce_plan(N, V, D, false);
+    constexpr bool kMany = Split<E>::kMany;
+    const CePlan p = ce_plan(N, V, D, kMany ? CSP_F32 : CSP_BF16, false, aligned(W, 16));
     int32_t *rows = (int32_t *)(w + p.rows), *count = (int32_t *)(w + p.count);
     float2 *part = (float2 *)(w + p.part);
     float *zt = (float *)(w + p.zt);
-    k_ce_rows<<<1, 1024, 0, s>>>(targets, N, V, rows, count);
-    CSP_LAUNCHED("k_ce_rows");
-    if (N > 0) {
-        k_ce_stats<E><<<dim3((unsigned)p.tiles, (unsigned)ceil_div(N, kTile)), kCeThreads, 0, s>>>(
-            (const T *)X, (const T *)W, targets, rows, count, N, V, D, part, zt);
+    csp_status st = ce_begin<E>(p, X, targets, N, V, D, loss, lse, w, s);
+    if (st != CSP_OK) return st;
+    for (int64_t v0 = 0; N > 0 && v0 < V; v0 += p.piece) {
+        Logits a;
+        st = ce_piece<E>(p, W, V, D, v0, w, &a, s);
+        if (st != CSP_OK) return st;
+        const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
+        if (p.bn == 64) k_ce_stats<64, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
+        else if (p.bn == 128) k_ce_stats<128, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
+        else k_ce_stats<256, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
         CSP_LAUNCHED("k_ce_stats");
-        k_ce_clear<<<(unsigned)ceil_div(N, 256), 256, 0, s>>>(N, loss, lse);
-        CSP_LAUNCHED("k_ce_clear");
-        k_ce_join<<<(unsigned)ceil_div(N, 64), 64, 0, s>>>(part, zt, rows, count, N, p.tiles, loss, lse);
+    }
+    if (N > 0) {
+        k_ce_join<<<(unsigned)ceil_div(N, 64), 1024, 0, s>>>(part, zt, rows, count, p.npad, p.tiles, loss, lse);
         CSP_LAUNCHED("k_ce_join");
     }
     k_ce_total<<<1, 1024, 0, s>>>(loss, count, N, total);
@@ -336,30 +619,40 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
                     hipStream_t s)
 {
     using T = typename E::T;
-    const CePlan p = ce_plan(N, V, D, true);
+    constexpr bool kMany = Split<E>::kMany;
+    const CePlan p = ce_plan(N, V, D, kMany ? CSP_F32 : CSP_BF16, true, aligned(W, 16));
     int32_t *rows = (int32_t *)(w + p.rows), *count = (int32_t *)(w + p.count);
-    float *P = (float *)(w + p.P), *acc = (float *)(w + p.acc);
-    k_ce_rows<<<1, 1024, 0, s>>>(targets, N, V, rows, count);
-    CSP_LAUNCHED("k_ce_rows");
-    const unsigned mt = (unsigned)ceil_div(N, kTile), ct = (unsigned)ceil_div(D, kTile);
-    if (N > 0) {
-        k_ce_dx_clear<E><<<(unsigned)N, kCeThreads, 0, s>>>(targets, V, D, (T *)dX);
-        CSP_LAUNCHED("k_ce_dx_clear");
-    }
+    uint16_t *P = (uint16_t *)(w + p.P);
+    const int64_t planep = p.npad * p.piece;
+    csp_status st = ce_begin<E>(p, X, targets, N, V, D, nullptr, nullptr, w, s);
+    if (st != CSP_OK) return st;
+    const int64_t per = round_up(ceil_div(p.piece, p.splits), kDepth);
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
-        const int64_t nv = V - v0 < p.piece ? V - v0 : p.piece;
-        const unsigned vt = (unsigned)ceil_div(nv, kTile);
+        Logits a;
+        st = ce_piece<E>(p, W, V, D, v0, w, &a, s);
+        if (st != CSP_OK) return st;
         if (N > 0) {
-            k_ce_probs<E><<<dim3(vt, mt), kCeThreads, 0, s>>>((const T *)X, (const T *)W, targets, lse, rows, count, V,
-                                                              D, v0, nv, P);
+            const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
+            if (p.bn == 64) k_ce_probs<64, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
+            else if (p.bn == 128) k_ce_probs<128, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
+            else k_ce_probs<256, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
             CSP_LAUNCHED("k_ce_probs");
-            k_ce_dx<E><<<dim3(ct, mt), kCeThreads, 0, s>>>(P, (const T *)W, rows, count, D, v0, nv, acc, v0 == 0,
-                                                           v0 + nv == V, dmean, total, (T *)dX);
+            const InputGrad d{P, a.W, p.piece, a.ldw, planep, a.planew, count, a.nv, D, p.splits, per,
+                              (float *)(w + p.acc), p.ldx, p.npad * p.ldx, v0 > 0};
+            const unsigned gx = (unsigned)(ceil_div(D, kBM) * ceil_div(N, p.bn) * p.splits);
+            if (p.bn == 64) k_ce_dx<64, kMany><<<gx, kTileThreads, 0, s>>>(d);
+            else if (p.bn == 128) k_ce_dx<128, kMany><<<gx, kTileThreads, 0, s>>>(d);
+            else k_ce_dx<256, kMany><<<gx, kTileThreads, 0, s>>>(d);
             CSP_LAUNCHED("k_ce_dx");
         }
-        k_ce_dw<E><<<dim3(ct, vt), kCeThreads, 0, s>>>(P, (const T *)X, rows, count, D, v0, nv, dmean, total,
-                                                            (T *)dW);
+        const WeightGrad g{P, a.X, p.piece, p.ldx, planep, a.planex, count, a.nv, D, dmean, total};
+        k_ce_dw<E><<<(unsigned)(ceil_div(D, kBM) * ceil_div(a.nv, 256)), kTileThreads, 0, s>>>(g, (T *)dW + v0 * D);
         CSP_LAUNCHED("k_ce_dw");
+    }
+    if (N > 0) {
+        k_ce_dx_out<E><<<(unsigned)N, kCeThreads, 0, s>>>((const float *)(w + p.acc), p.ldx, p.npad * p.ldx, p.splits,
+                                                          (const int32_t *)(w + p.slot), D, dmean, total, (T *)dX);
+        CSP_LAUNCHED("k_ce_dx_out");
     }
     return CSP_OK;
 }
@@ -372,7 +665,7 @@ extern "C" {
 int64_t linear_ce_workspace(int64_t N, int64_t V, int64_t D, csp_dtype dtype, int32_t backward)
 {
     if (csp::ce_args(N, V, D, dtype) != CSP_OK) return -1;
-    return (int64_t)csp::ce_plan(N, V, D, backward != 0).total;
+    return (int64_t)csp::ce_bytes(N, V, D, dtype, backward != 0);
 }
 
 csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
@@ -386,7 +679,7 @@ csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, i
     if (!aligned(W, e) || !aligned(total, 4) ||
         (N > 0 && (!aligned(X, e) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4))))
         return set_error(CSP_ERR_INVALID_ARG, "NULL or misaligned pointer");
-    const size_t need = ce_plan(N, V, D, false).total;
+    const size_t need = ce_bytes(N, V, D, dtype, false);
     if (!aligned(workspace, 16) || workspace_bytes < (int64_t)need)
         return set_error(CSP_ERR_INVALID_ARG, "workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
     if (dtype == CSP_BF16)
@@ -405,7 +698,7 @@ csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, i
     if (!aligned(W, e) || !aligned(dW, e) || !aligned(dmean, 4) || !aligned(total, 4) ||
         (N > 0 && (!aligned(X, e) || !aligned(targets, 8) || !aligned(lse, 4) || !aligned(dX, e))))
         return set_error(CSP_ERR_INVALID_ARG, "NULL or misaligned pointer");
-    const size_t need = ce_plan(N, V, D, true).total;
+    const size_t need = ce_bytes(N, V, D, dtype, true);
     if (!aligned(workspace, 16) || workspace_bytes < (int64_t)need)
         return set_error(CSP_ERR_INVALID_ARG, "workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
     if (dtype == CSP_BF16)

@@ -277,10 +277,6 @@ __global__ __launch_bounds__(1024) void k_ce_total(const float *__restrict__ los
 
 // A wave's tile goes out through its own part of LDS, so that stores cover whole row segments: FN *
 // 16 output rows (n) of TM elements (m), 16 bytes of padding a row against bank conflicts.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-struct __attribute__((packed, aligned(2))) Vec16 {
-    u32x4 v;
-};
 template <int TM, int kRows, typename O>
 struct Stage {
     static constexpr int kStride = TM * (int)sizeof(O) + 16;
@@ -296,7 +292,7 @@ struct Stage {
             if (r >= rows || e >= cols) continue;
             const u32x4 v = *(const u32x4 *)(mine + r * kStride + (l % kLanes) * 16);
             O *p = out + r * ld + e;
-            if (e + kPer <= cols) ((Vec16 *)p)->v = v;
+            if (e + kPer <= cols) store16(p, v);
             else
                 for (int k = 0; e + k < cols; ++k) p[k] = ((const O *)(mine + r * kStride))[e + k];
         }

@@ -33,12 +33,6 @@ struct InlineTable {
     Entry e[kInline];
 };
 
-// Any alignment the element type allows: buckets are split at odd offsets.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-struct __attribute__((packed, aligned(2))) Vec16 {
-    u32x4 v;
-};
-
 __global__ void k_table_put(InlineTable t, int n, Entry *__restrict__ dst)
 {
     if ((int)threadIdx.x < n) dst[threadIdx.x] = t.e[threadIdx.x];
@@ -86,7 +80,7 @@ __device__ __forceinline__ double square_chunk(const Entry &t, int64_t chunk)
     for (int j = 0; j < kVecPerThread; ++j) {
         const int64_t i = base + (int64_t)(j * kClipThreads + threadIdx.x) * per;
         v[j] = u32x4{0u, 0u, 0u, 0u};
-        if (i + per <= t.n) v[j] = ((const Vec16 *)(g + (bf ? 2 : 4) * i))->v;
+        if (i + per <= t.n) v[j] = load16(g + (bf ? 2 : 4) * i);
         else if (i < t.n) {  // the tensor's end: element by element
             for (int64_t k = i; k < t.n; ++k) {
                 const double x = bf ? (double)BF16::load((const uint16_t *)g, k) : (double)((const float *)g)[k];
@@ -157,7 +151,7 @@ __device__ __forceinline__ void scale_chunk(const Entry &t, int64_t chunk, float
     for (int j = 0; j < kVecPerThread; ++j) {
         const int64_t i = base + (int64_t)(j * kClipThreads + threadIdx.x) * per;
         v[j] = u32x4{0u, 0u, 0u, 0u};
-        if (i + per <= t.n) v[j] = ((const Vec16 *)(g + (bf ? 2 : 4) * i))->v;
+        if (i + per <= t.n) v[j] = load16(g + (bf ? 2 : 4) * i);
     }
 #pragma unroll
     for (int j = 0; j < kVecPerThread; ++j) {
@@ -173,7 +167,7 @@ __device__ __forceinline__ void scale_chunk(const Entry &t, int64_t chunk, float
                     v[j][q] = __float_as_uint(__uint_as_float(v[j][q]) * c);
                 }
             }
-            ((Vec16 *)(o + (bf ? 2 : 4) * i))->v = v[j];
+            store16(o + (bf ? 2 : 4) * i, v[j]);
         } else if (i < t.n) {
             for (int64_t k = i; k < t.n; ++k) {
                 if (bf) ((uint16_t *)o)[k] = BF16::from_f(BF16::load((const uint16_t *)g, k) * c);

@@ -64,6 +64,17 @@ struct BF16 {
         return (uint16_t)(u >> 16);
     }
 };
+
+// 16 bytes at any alignment that the element type allows (rows of odd widths and slices of larger
+// tensors start there); the memory system takes such accesses whole.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+struct __attribute__((packed, aligned(2))) Vec16 {
+    u32x4 v;
+};
+__device__ __forceinline__ u32x4 load16(const void *p) { return ((const Vec16 *)p)->v; }
+__device__ __forceinline__ void store16(void *p, u32x4 v) { ((Vec16 *)p)->v = v; }
+__device__ __forceinline__ void store16_nt(void *p, u32x4 v) { __builtin_nontemporal_store(v, &((Vec16 *)p)->v); }  // not kept in L2
+
 // Lanes of the wave whose 8-bit value d equals this lane's, among the lanes
 // with `take` set (eight ballots, one per bit).
 __device__ __forceinline__ uint64_t lanes_with_same_byte(uint32_t d, bool take)

@@ -182,6 +182,32 @@ def test_embed(N, V, D, how, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V,D,how", [
+    (70001, 65536, 8, "skewed"), (150_000, 40_000, 5, "uniform"), (33_000, 200_000, 9, "one"),   # sorted by digits
+    (3, 17_000_000, 1, "uniform"), (0, 17_000_000, 2, "uniform"),                                # a very long table
+    (64, 9, 31, "one"), (65, 9, 31, "one"), (128, 9, 31, "one"), (129, 300, 516, "one"),         # whole pieces of an id
+    (5000, 3, 260, "uniform"), (2049, 256, 2056, "skewed"), (900, 512, 7, "skewed"), (40, 513, 2, "skewed")])
+def test_embed_paths(N, V, D, how, dtype):
+    """Both sorts, ids of many tokens cut into pieces at and around the cuts, tables of several id ranges."""
+    test_embed(N, V, D, how, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lead", [0, 1, 37, 63])
+def test_embed_long_ids_between_short_ones(lead):
+    """Pieces of ids of 63 to 200 tokens that begin anywhere between the cuts, exact in integers."""
+    sizes = [lead, 64, 65, 1, 63, 128, 129, 0, 200, 3, 66]
+    ids = torch.repeat_interleave(torch.arange(len(sizes)), torch.tensor(sizes)).cuda()
+    ids = ids[torch.randperm(ids.numel(), generator=torch.Generator().manual_seed(lead)).cuda()]
+    dY = torch.randint(-8, 9, (ids.numel(), 20), generator=gen(lead), device="cuda").float()
+    want = torch.zeros(len(sizes) + 2, 20, dtype=torch.float64, device="cuda").index_add_(0, ids, dY.double())
+    assert torch.equal(csp.embed_bwd(dY, ids, len(sizes) + 2).double(), want)
+    got = csp.embed_bwd(dY.bfloat16(), ids, len(sizes) + 2)
+    assert torch.equal(got, want.float().bfloat16())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_embed_at_element_alignment(dtype):
     """Tables, gradients and outputs that start one element past a 16-byte boundary."""
     N, V, D = 70, 40, 96

@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libcoospmm.so")
 SOURCES = ["layer.hip", "build.hip", "sort.hip", "spmm.hip", "restructure.hip", "occupancy.hip",
-           "embed.hip", "ce.hip", "clip.hip"]
+           "embed.hip", "ce.hip", "ce_few.hip", "clip.hip"]
 ARCH = "gfx950"
 
 

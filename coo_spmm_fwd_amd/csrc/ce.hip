@@ -26,6 +26,7 @@
 // term at most, is that of the rounding of the outputs, and the scale dmean /
 // count is applied to the fp32 sums after it.  In fp32, X, W and P are split
 // into three bf16 planes (mfma_tile.h).
+#include "ce.h"
 #include "mfma_tile.h"
 
 namespace csp {
@@ -34,12 +35,6 @@ namespace {
 constexpr int kCeThreads = 256;
 constexpr int kBM = 256;       // vocabulary rows (or columns of X) of a tile
 constexpr int64_t kPad = 256;  // token and vocabulary strides are multiples of it
-constexpr float kLog2e = 1.44269504088896340736f;
-
-__host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
-
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
-
 // fp32 or bf16 elements as bf16 planes.
 template <typename E> struct Split;
 template <> struct Split<BF16> {
@@ -395,12 +390,6 @@ __global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_dx(Inp
     }
 }
 
-// dmean / count, with the count that the forward divided by.
-__device__ __forceinline__ float grad_scale(const float *dmean, const float *total)
-{
-    return dmean[0] / fmaxf(total[1], 1.0f);
-}
-
 // dX[n] = the splits' sums of its place in the list, scaled and rounded; zeros if it has none.
 template <typename E>
 __global__ __launch_bounds__(kCeThreads) void k_ce_dx_out(const float *__restrict__ acc, int64_t lda, int64_t plane,
@@ -530,14 +519,15 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
 
 size_t ce_bytes(int64_t N, int64_t V, int64_t D, int dtype, bool backward)
 {
+    if (N <= kFewTokens) return ce_few_bytes(N, V, D, dtype, backward);
     const size_t a = ce_plan(N, V, D, dtype, backward, true).total, b = ce_plan(N, V, D, dtype, backward, false).total;
     return a > b ? a : b;
 }
 
 csp_status ce_args(int64_t N, int64_t V, int64_t D, int dtype)
 {
-    constexpr int64_t kLimit = 0x7FFFFFFF - kPad;
-    if (N < 0 || N >= kLimit || V < 1 || V >= kLimit || D < 1 || D >= (int64_t)1 << 22)  // 2^22: 32-bit offsets in a tile
+    // a launch has fewer than 2^32 threads (256 a token, 2 a vocabulary row); 32-bit offsets in a tile
+    if (N < 0 || N >= (int64_t)1 << 24 || V < 1 || V > (int64_t)1 << 30 || D < 1 || D >= (int64_t)1 << 22)
         return set_error(CSP_ERR_INVALID_ARG, "bad shape: %lld tokens, vocabulary %lld, width %lld", (long long)N,
                          (long long)V, (long long)D);
     if (dtype != CSP_F32 && dtype != CSP_BF16) return set_error(CSP_ERR_DTYPE, "unsupported dtype %d", dtype);
@@ -678,6 +668,8 @@ csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, i
     const size_t need = ce_bytes(N, V, D, dtype, false);
     if (!aligned(workspace, 16) || workspace_bytes < (int64_t)need)
         return set_error(CSP_ERR_INVALID_ARG, "workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
+    if (N <= kFewTokens)
+        return ce_few_fwd(X, W, targets, N, V, D, dtype, loss, lse, total, (char *)workspace, (hipStream_t)stream);
     if (dtype == CSP_BF16)
         return fwd_impl<BF16>(X, W, targets, N, V, D, loss, lse, total, (char *)workspace, (hipStream_t)stream);
     return fwd_impl<F32>(X, W, targets, N, V, D, loss, lse, total, (char *)workspace, (hipStream_t)stream);
@@ -697,6 +689,8 @@ csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, i
     const size_t need = ce_bytes(N, V, D, dtype, true);
     if (!aligned(workspace, 16) || workspace_bytes < (int64_t)need)
         return set_error(CSP_ERR_INVALID_ARG, "workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
+    if (N <= kFewTokens)
+        return ce_few_bwd(X, W, targets, N, V, D, dtype, lse, dmean, total, dX, dW, (char *)workspace, (hipStream_t)stream);
     if (dtype == CSP_BF16)
         return bwd_impl<BF16>(X, W, targets, N, V, D, lse, dmean, total, dX, dW, (char *)workspace, (hipStream_t)stream);
     return bwd_impl<F32>(X, W, targets, N, V, D, lse, dmean, total, dX, dW, (char *)workspace, (hipStream_t)stream);

@@ -384,7 +384,7 @@ csp_status sparse_layer_time_next(sparse_layer_t layer, void *ev_before, void *e
  * says, contents undefined before and after).  All are asynchronous on
  * "stream", allocate nothing and may be captured in a HIP graph.  No float
  * result depends on the order of atomics: the same inputs give the same bits.
- * Limits: N, V, D < 2^31; N = 0 is valid.  The _workspace functions return -1
+ * Limits: N, V, D < 2^31 (linear_ce: N < 2^24, V <= 2^30, D < 2^22); N = 0 is valid.  The _workspace functions return -1
  * for arguments that the call would refuse.
  */
 

@@ -334,6 +334,20 @@ def test_linear_ce(N, V, D, mask, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V,D,mask", [(1, 127, 65, "none"), (3, 128, 2100, "some"), (15, 129, 127, "none"),
+                                        (16, 31, 1001, "some"), (17, 4097, 768, "some"), (32, 33, 513, "last"),
+                                        (40, 700, 2100, "some"), (48, 2049, 36, "all"), (64, 12800, 1024, "some"),
+                                        (64, 5, 4100, "none"), (64, 40, 7, "some"), (61, 9001, 129, "some")])
+def test_linear_ce_few_tokens(N, V, D, mask, dtype):
+    """Up to 64 tokens: parts of a wave's 32 and a workgroup's 128 vocabulary rows, chunks and groups of columns
+    that end inside or at a 16-byte load."""
+    got = ce_check(*ce_inputs(N, V, D, dtype, N + 3 * V + D, mask))
+    if mask == "all":
+        assert not got["dX"].any() and not got["dW"].any() and not got["total"].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_linear_ce_over_several_pieces(dtype):
     """So many logits that the backward goes over the vocabulary in pieces."""
     ce_check(*ce_inputs(3000, 66001, 24, dtype, 9, "some"))

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_uint64, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -140,8 +141,9 @@ def _torch():
 
 
 def _stream(stream):
-    if stream is None:
-        return c_void_p(_torch().cuda.current_stream().cuda_stream)
+    if stream is None:  # the current stream's handle without a Stream object around it
+        torch = _torch()
+        return c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return c_void_p(stream)
     return c_void_p(stream.cuda_stream)
@@ -494,14 +496,12 @@ def _work(nbytes: int, device, stream):
 
 
 def _device(*tensors):
-    """The one device of all tensors, which has to be the current one (its stream is used)."""
+    """All tensors have to be on the current device (its stream is used)."""
     torch = _torch()
-    d = tensors[0].device
-    if any(t.device != d for t in tensors):
-        raise ValueError("tensors are on different devices")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {d}, which is not the current device")
-    return d
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t.get_device() != here:
+            raise ValueError(f"a tensor is on {t.device}, which is not the current device")
 
 
 def _matrix(t, name, dtype=None):
@@ -591,25 +591,35 @@ def linear_ce_bwd(X, W, targets, lse, dmean, total, dX=None, dW=None, stream=Non
 def _tensor_list(ts, name, like=None):
     """Host arrays of pointers, element counts and dtype codes of a list of GPU tensors."""
     torch = _torch()
-    codes = {torch.float32: CSP_F32, torch.bfloat16: CSP_BF16}
     n = len(ts)
+    if like is not None and len(like[0]) != n:
+        raise ValueError(f"{n} {name} for {len(like[0])} gradients")
+    codes = {torch.float32: CSP_F32, torch.bfloat16: CSP_BF16}
+    here = torch.cuda.current_device() if n and ts[0].is_cuda else -1
+    ptrs, sizes, types = array("Q"), array("q"), array("i")
     for t in ts:
-        if not t.is_cuda:
-            raise TypeError(f"{name} must be GPU tensors")
+        if t.get_device() != here or here < 0:
+            if not t.is_cuda:
+                raise TypeError(f"{name} must be GPU tensors")
+            raise ValueError(f"a tensor is on {t.device}, which is not the current device")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.dtype not in codes:
+        code = codes.get(t.dtype)
+        if code is None:
             raise TypeError(f"unsupported dtype {t.dtype}")
-    if like is not None:
-        if len(like) != n:
-            raise ValueError(f"{n} {name} for {len(like)} gradients")
-        for t, g in zip(ts, like):
-            if t.dtype != g.dtype or t.numel() != g.numel():
-                raise ValueError(f"{name} must have the gradients' types and sizes")
-    if n:
-        _device(*ts)
-    return ((c_void_p * n)(*[t.data_ptr() for t in ts]), (c_int64 * n)(*[t.numel() for t in ts]),
-            (c_int32 * n)(*[codes[t.dtype] for t in ts]))
+        ptrs.append(t.data_ptr())
+        sizes.append(t.numel())
+        types.append(code)
+    if like is not None and (sizes != like[1] or types != like[2]):
+        raise ValueError(f"{name} must have the gradients' types and sizes")
+    return ptrs, sizes, types
+
+
+def _host_arrays(ts):
+    """ctypes views of what _tensor_list returned."""
+    ptrs, sizes, types = ts
+    n = len(ptrs)
+    return (c_void_p * n).from_buffer(ptrs), (c_int64 * n).from_buffer(sizes), (c_int32 * n).from_buffer(types)
 
 
 def _norm_out(grads, norm, stream):
@@ -624,7 +634,7 @@ def _norm_out(grads, norm, stream):
 def grad_norm(grads, norm=None, stream=None):
     """The 2-norm of all elements of a list of fp32 and bf16 tensors, as an fp32 tensor [1]."""
     grads = list(grads)
-    gp, nn, dt = _tensor_list(grads, "grads")
+    gp, nn, dt = _host_arrays(_tensor_list(grads, "grads"))
     L, w, norm, np_ = _norm_out(grads, norm, stream)
     _check(L.grad_norm(gp, nn, dt, len(grads), np_, c_void_p(w.data_ptr()), w.numel(), _stream(stream)))
     return norm
@@ -634,8 +644,9 @@ def grad_clip(grads, max_norm: float, outs=None, norm=None, stream=None):
     """Multiply every tensor by min(1, max_norm / (norm + 1e-6)), in place or into `outs`; returns
     the norm before clipping, as an fp32 tensor [1] (nothing is read back to the host)."""
     grads = list(grads)
-    gp, nn, dt = _tensor_list(grads, "grads")
-    op = gp if outs is None else _tensor_list(list(outs), "outs", grads)[0]
+    mine = _tensor_list(grads, "grads")
+    gp, nn, dt = _host_arrays(mine)
+    op = gp if outs is None else _host_arrays(_tensor_list(list(outs), "outs", mine))[0]
     L, w, norm, np_ = _norm_out(grads, norm, stream)
     _check(L.grad_clip(gp, op, nn, dt, len(grads), float(max_norm), np_, c_void_p(w.data_ptr()), w.numel(),
                        _stream(stream)))

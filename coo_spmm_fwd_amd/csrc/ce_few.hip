@@ -222,7 +222,10 @@ __global__ __launch_bounds__(kFewThreads) void k_few_prep(const typename E::T *_
 // ---------------------------------------------------------------------------
 // 128 vocabulary rows a workgroup.  The rows of a wave arrive 4 loads ahead in
 // registers (8 KiB a wave), the tokens' fragments of a chunk through LDS (two
-// buffers, one barrier a chunk).
+// buffers, one barrier a chunk).  Workgroups begin at different chunks: all rows
+// are in work at once, and with a common stride their reads of one chunk meet
+// in the same memory channels (one token, 65536 x 4096 bf16: 136 us in step, 99
+// us, 5.4 TB/s, apart).
 // ---------------------------------------------------------------------------
 struct FewArgs {
     const int32_t *rows, *tgt, *count;
@@ -236,7 +239,7 @@ struct FewArgs {
     u32x4 *Pf;     // [vocabulary / 32][block][plane]: rows 16 tokens, depth 32 vocabulary rows 8 q + j
 };
 
-template <typename E, int NB, bool kBackward>
+template <typename E, int NB, bool kBackward, bool kStream>
 __global__ __launch_bounds__(kFewThreads, 2) void k_few_rows(FewArgs a, const typename E::T *__restrict__ W,
                                                              typename E::T *__restrict__ dW)
 {
@@ -264,11 +267,13 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_few_rows(FewArgs a, const ty
 #pragma unroll
         for (int t = 0; t < NB; ++t) acc[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     const int chunks = (int)((D + kChunk<E> - 1) / kChunk<E>);
+    const int turn = (int)((blockIdx.x >> 3) % (unsigned)chunks);
+    auto chunk_of = [&](int c) { return c + turn < chunks ? c + turn : c + turn - chunks; };
     auto load_x = [&](int c, u32x4 (&x)[kXLoads]) {
 #pragma unroll
         for (int i = 0; i < kXLoads; ++i) {
             const int e = i * kFewThreads + tid;
-            x[i] = a.Xf[(int64_t)c * kXChunk + (e < kXChunk ? e : 0)];
+            x[i] = a.Xf[(int64_t)chunk_of(c) * kXChunk + (e < kXChunk ? e : 0)];
         }
     };
     auto put_x = [&](int c, const u32x4 (&x)[kXLoads]) {
@@ -279,14 +284,16 @@ __global__ __launch_bounds__(kFewThreads, 2) void k_few_rows(FewArgs a, const ty
         }
     };
     auto load_w = [&](int c, u32x4 (&r)[2][4]) {
-        const int64_t k = (int64_t)c * kChunk<E> + (kPer == 8 ? 8 : 4) * q;
-        const bool whole = (int64_t)(c + 1) * kChunk<E> <= D;
+        const int64_t k0 = (int64_t)chunk_of(c) * kChunk<E>, k = k0 + kPer * q;
+        const bool whole = k0 + kChunk<E> <= D;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t e = k + i * (kPer == 8 ? 32 : 16);
-                r[b][i] = whole ? load16(row[b] + e) : load_edge<E>(row[b], e, D);
+                if (!whole) r[b][i] = load_edge<E>(row[b], e, D);
+                else if constexpr (kStream) r[b][i] = load16_nt(row[b] + e);
+                else r[b][i] = load16(row[b] + e);
             }
     };
     auto multiply = [&](int c, const u32x4 (&r)[2][4]) {
@@ -767,7 +774,7 @@ csp_status fwd_few(const void *X, const void *W, const int64_t *targets, int64_t
     a.part = (float2 *)(w + p.part);
     a.zt = (float *)(w + p.zt);
     if (N > 0) {
-        k_few_rows<E, NB, false><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const typename E::T *)W, nullptr);
+        k_few_rows<E, NB, false, false><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const typename E::T *)W, nullptr);
         CSP_LAUNCHED("k_few_rows");
     }
     k_few_join<NB><<<1, 1024, 0, s>>>(a.part, a.zt, a.rows, a.count, N > 0 ? p.tiles : 0, loss, lse, total);
@@ -788,7 +795,12 @@ csp_status bwd_few(const void *X, const void *W, const int64_t *targets, int64_t
     a.dmean = dmean;
     a.total = total;
     a.Pf = (u32x4 *)(w + p.Pf);
-    k_few_rows<E, NB, true><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
+    // A W past the memory-side cache (256 MB) is not there for k_few_dx anyway, and streaming it leaves the
+    // cache to dW (64 tokens, 537 MB: 546 / 513 us a step plain / streamed; 154 MB: 177 / 190).
+    if (V * D * (int64_t)sizeof(T) > (int64_t)256 << 20)
+        k_few_rows<E, NB, true, true><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
+    else
+        k_few_rows<E, NB, true, false><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
     CSP_LAUNCHED("k_few_rows");
     if (N == 0) return CSP_OK;
     const FewDx d{a.Pf, V, D, p.splits, p.per, (float *)(w + p.acc), p.lda, 16 * NB * p.lda};

@@ -72,6 +72,7 @@ struct __attribute__((packed, aligned(2))) Vec16 {
     u32x4 v;
 };
 __device__ __forceinline__ u32x4 load16(const void *p) { return ((const Vec16 *)p)->v; }
+__device__ __forceinline__ u32x4 load16_nt(const void *p) { return __builtin_nontemporal_load(&((const Vec16 *)p)->v); }
 __device__ __forceinline__ void store16(void *p, u32x4 v) { ((Vec16 *)p)->v = v; }
 __device__ __forceinline__ void store16_nt(void *p, u32x4 v) { __builtin_nontemporal_store(v, &((Vec16 *)p)->v); }  // not kept in L2
 

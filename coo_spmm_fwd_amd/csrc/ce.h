@@ -13,11 +13,87 @@ __host__ __device__ inline int64_t round_up(int64_t a, int64_t b) { return (a + 
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// exp(x - b) from b log2 e: one operation less, and off by the rounding of b log2 e, which is that of b.
+__device__ __forceinline__ float exp_less(float x, float b2) { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -b2)); }
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)  // round to nearest even
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+__device__ __forceinline__ float low_of(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float high_of(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+
+// Two floats as three pairs of bf16, x = x0 + x1 + x2: each the rest rounded to nearest.  Values past the
+// largest bf16 leave the excess to the second plane.  An infinity ends as NaN (infinity less infinity).
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[3])
+{
+    constexpr float kMax = 3.38953139e38f;
+    p[0] = pack_bf16(__builtin_amdgcn_fmed3f(a, -kMax, kMax), __builtin_amdgcn_fmed3f(b, -kMax, kMax));
+    a -= low_of(p[0]);
+    b -= high_of(p[0]);
+    p[1] = pack_bf16(a, b);
+    p[2] = pack_bf16(a - low_of(p[1]), b - high_of(p[1]));
+}
+
 // dmean / count, with the count that the forward divided by.
 __device__ __forceinline__ float grad_scale(const float *dmean, const float *total)
 {
     return dmean[0] / fmaxf(total[1], 1.0f);
 }
+
+namespace {
+// dX[n] = the sum of the splits' rows of its place in the list (acc[split][place][lda], lda a multiple of
+// 4), scaled and rounded; zeros if it has none.  One thread for 4 columns.
+template <typename E>
+__global__ __launch_bounds__(256) void k_ce_out(const float *__restrict__ acc, int64_t lda, int64_t plane, int splits,
+                                                const int32_t *__restrict__ slot, int64_t N, int64_t D,
+                                                const float *__restrict__ dmean, const float *__restrict__ total,
+                                                typename E::T *__restrict__ dX)
+{
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    constexpr int kAhead = 8;
+    const int64_t groups = (D + 3) / 4, all = N * groups;
+    const float scale = grad_scale(dmean, total);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int64_t n = i / groups, c = (i - n * groups) * 4;
+        const int m = slot[n];
+        f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
+        if (m >= 0) {
+            const float *p = acc + m * lda + c;
+            int k = 0;
+            for (; k + kAhead <= splits; k += kAhead) {
+                f32x4 x[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) x[j] = *(const f32x4 *)(p + (k + j) * plane);
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) s += x[j];
+            }
+            for (; k < splits; ++k) s += *(const f32x4 *)(p + k * plane);
+            s *= scale;
+        }
+        if (c + 4 <= D) {
+            if constexpr (sizeof(typename E::T) == 4) {
+                store16(dX + n * D + c, __builtin_bit_cast(u32x4, s));
+            } else {
+                struct __attribute__((packed, aligned(2))) Two {
+                    uint32_t a, b;
+                };
+                *(Two *)(dX + n * D + c) = Two{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+            }
+        } else {
+            for (int k = 0; c + k < D; ++k) dX[n * D + c + k] = E::from_f(s[k]);
+        }
+    }
+}
+inline unsigned out_blocks(int64_t N, int64_t D)
+{
+    const int64_t b = (N * ((D + 3) / 4) + 255) / 256;
+    return (unsigned)(b < 65536 ? b : 65536);
+}
+}  // namespace
 
 constexpr int64_t kFewTokens = 64;
 size_t ce_few_bytes(int64_t N, int64_t V, int64_t D, int dtype, bool backward);

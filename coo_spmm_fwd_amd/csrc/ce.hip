@@ -22,7 +22,7 @@
 //   logits  m = vocabulary, n = token,      k = width       (W and X by rows)
 //   dX      m = width,      n = token,      k = vocabulary  (W by depth, P by rows)
 //   dW      m = width,      n = vocabulary, k = token       (X and P by depth)
-// In bf16, P is rounded to bf16 to enter the products: its error, 2^-9 of each
+// In bf16, P is rounded to bf16 to enter the products: its error, 2^-8 of each
 // term at most, is that of the rounding of the outputs, and the scale dmean /
 // count is applied to the fp32 sums after it.  In fp32, X, W and P are split
 // into three bf16 planes (mfma_tile.h).
@@ -43,17 +43,6 @@ template <> struct Split<BF16> {
 template <> struct Split<F32> {
     static constexpr bool kMany = true;
 };
-// The next plane of x: x rounded to bf16, x left with the rest.  An infinity or NaN goes whole into
-// the first plane; a finite value that would round to infinity is cut to the largest bf16 instead.
-__device__ __forceinline__ uint16_t take_plane(float &x)
-{
-    uint16_t p = BF16::from_f(x);
-    const bool finite = (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
-    if (finite && (p & 0x7FFFu) == 0x7F80u) p -= 1;
-    x = finite ? x - __uint_as_float((uint32_t)p << 16) : 0.0f;
-    return p;
-}
-
 // Tokens that take part, in order: rows[0 .. count) and their targets tgt; slot[n] = place in that
 // list, or -1.  Clears loss and lse (if given) of the others.  One workgroup.
 __global__ __launch_bounds__(1024) void k_ce_rows(const int64_t *__restrict__ targets, int64_t N, int64_t V,
@@ -98,19 +87,46 @@ __global__ __launch_bounds__(kCeThreads) void k_ce_gather(const typename E::T *_
         real = r < cnt;
     }
     const int64_t from = real ? (rows ? rows[r] : r) : 0;
-    for (int64_t c = threadIdx.x; c < ld; c += kCeThreads) {
+    for (int64_t c = threadIdx.x * 8; c < ld; c += kCeThreads * 8) {  // ld is a multiple of 64
+        const typename E::T *p = src + from * D + c;
+        u32x4 out[kPlanes];
         if constexpr (Split<E>::kMany) {
-            float x = real && c < D ? E::load(src, from * D + c) : 0.0f;
+            float x[8];
+            if (real && c + 8 <= D) {
 #pragma unroll
-            for (int p = 0; p < kPlanes; ++p) dst[p * plane + r * ld + c] = take_plane(x);
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 v = load16(p + 4 * h);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[4 * h + i] = __uint_as_float(v[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = real && c + i < D ? p[i] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t q[kPlanes];
+                split_pair(x[2 * i], x[2 * i + 1], q);
+#pragma unroll
+                for (int k = 0; k < kPlanes; ++k) out[k][i] = q[k];
+            }
         } else {
-            dst[r * ld + c] = real && c < D ? src[from * D + c] : (uint16_t)0;
+            out[0] = u32x4{0u, 0u, 0u, 0u};
+            if (real && c + 8 <= D) {
+                out[0] = load16(p);
+            } else if (real) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < D) out[0][i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+            }
         }
+#pragma unroll
+        for (int k = 0; k < (Split<E>::kMany ? kPlanes : 1); ++k) *(u32x4 *)(dst + k * plane + r * ld + c) = out[k];
     }
 }
 
 // The place of a workgroup in a grid of mt x nt tiles (and `splits` of the depth).  Workgroups go
-// round the 8 XCDs; each XCD takes one contiguous run of tiles, walked in columns 8 tiles wide, so
+// round the 8 XCDs; each XCD takes one contiguous run of tiles, walked in columns 4 tiles wide, so
 // that the tiles an XCD holds at a time share operands in its L2.
 struct TilePlace {
     int64_t m, n, split;
@@ -125,17 +141,15 @@ __device__ __forceinline__ TilePlace tile_place(int64_t mt, int64_t nt, int64_t 
     int64_t id = x * q + (x < r ? x : r) + (b >> 3);
     t.split = id / (mt * nt);
     id -= t.split * (mt * nt);
-    const int64_t grp = id / (mt * 8), rem = id - grp * mt * 8, width = nt - grp * 8 < 8 ? nt - grp * 8 : 8;
+    const int64_t grp = id / (mt * 4), rem = id - grp * mt * 4, width = nt - grp * 4 < 4 ? nt - grp * 4 : 4;
     t.m = rem / width;
-    t.n = grp * 8 + rem % width;
+    t.n = grp * 4 + rem % width;
     return t;
 }
 
-// Waves of a tile with BN tokens: 256 x 256 by 2 x 4, 256 x 128 by 4 x 2, 256 x 64 by 8 x 1.
-template <int BN> struct Waves {
-    static constexpr int kM = BN == 256 ? 2 : BN == 128 ? 4 : 8, kN = kTileWaves / kM;
-    static constexpr int kPerSimd = BN == 64 ? 4 : 2;  // two workgroups a CU where LDS holds them
-};
+// Waves of a tile of 256 x BN: 2 x 4, or 4 x 2 for 128 tokens.
+template <int BN> constexpr int kWavesM = BN == 256 ? 2 : 4;
+template <int BN> constexpr int kWavesN = kTileWaves / kWavesM<BN>;
 
 struct Logits {
     const uint16_t *X, *W;  // planes: listed tokens [.][ldx], vocabulary rows of the piece [.][ldw]
@@ -160,10 +174,10 @@ __device__ __forceinline__ bool logits_tile(const Logits &a, T &tile, TilePlace 
 
 // Per (vocabulary tile, listed token): maximum and sum of exp(z - maximum); the target's logit.
 template <int BN, bool kMany>
-__global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_stats(Logits a, float2 *__restrict__ part,
+__global__ __launch_bounds__(kTileThreads, 2) void k_ce_stats(Logits a, float2 *__restrict__ part,
                                                                                 float *__restrict__ zt)
 {
-    using T = Tile<false, false, kBM, BN, Waves<BN>::kM, Waves<BN>::kN>;
+    using T = Tile<false, false, kBM, BN, kWavesM<BN>, kWavesN<BN>>;
     __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
     T tile;
     TilePlace at;
@@ -171,36 +185,44 @@ __global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_stats(
     const int l = threadIdx.x & 63, g = l >> 4, wm = T::wave_m(), wn = T::wave_n();
     const int64_t cnt = a.count[0], vw = at.m * kBM + wm * (16 * T::FM);  // the wave's first row of the piece
     float2 *join = (float2 *)smem;                                        // [wave row][BN]
-    const bool edge = at.m * kBM + kBM > a.nv;
+    const int valid = (int)(a.nv - vw < 16 * T::FM ? a.nv - vw : 16 * T::FM) - 4 * g;  // rows from the lane's first on
+    const bool edge = a.nv - vw < 16 * T::FM;
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {
         const int nl = (wn * T::FN + j) * 16 + (l & 15);
         const int64_t n = at.n * BN + nl;
-        const int64_t t = n < cnt ? a.tgt[n] - a.v0 - vw - 4 * g : -1;  // relative to the lane's first row
-        float mx = -INFINITY, z = 0.0f;
-        bool hit = false;
+        float x[T::FM][4], mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < T::FM; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                float x = tile.acc[i][j][r];
-                if (edge && vw + 16 * i + 4 * g + r >= a.nv) x = -INFINITY;
-                tile.acc[i][j][r] = x;
-                if (t == 16 * i + r) {
-                    z = x;
-                    hit = true;
-                }
-                mx = fmaxf(mx, x);
+                x[i][r] = tile.acc[i][j][r];
+                if (edge) x[i][r] = 16 * i + r >= valid ? -INFINITY : x[i][r];
             }
-        if (hit) zt[n] = z;
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[i][r]);
+        // the target's logit: few waves hold one
+        const int64_t t64 = n < cnt ? a.tgt[n] - a.v0 - vw - 4 * g : -1;
+        const int t = t64 >= 0 && t64 < 16 * T::FM && (t64 & 12) == 0 ? (int)t64 : -1;
+        if (__ballot(t >= 0) != 0) {
+            float z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) z = t == 16 * i + r ? x[i][r] : z;
+            if (t >= 0) zt[n] = z;
+        }
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         const float base = mx == -INFINITY ? 0.0f : mx;  // nothing of the vocabulary in this wave
+        const float base2 = base * kLog2e;
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s += exp_of(tile.acc[i][j][r] - base);
+            for (int r = 0; r < 4; ++r) s += exp_less(x[i][r], base2);
         s += __shfl_xor(s, 16, 64);
         s += __shfl_xor(s, 32, 64);
         if (g == 0) join[wm * BN + nl] = make_float2(mx, s);
@@ -210,9 +232,9 @@ __global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_stats(
         const int64_t n = at.n * BN + nl;
         if (n >= cnt) continue;
         float mx = join[nl].x, s = 0.0f;
-        for (int w = 1; w < Waves<BN>::kM; ++w) mx = fmaxf(mx, join[w * BN + nl].x);
+        for (int w = 1; w < kWavesM<BN>; ++w) mx = fmaxf(mx, join[w * BN + nl].x);
         const float base = mx == -INFINITY ? 0.0f : mx;
-        for (int w = 0; w < Waves<BN>::kM; ++w)
+        for (int w = 0; w < kWavesM<BN>; ++w)
             s += join[w * BN + nl].y * exp_of(join[w * BN + nl].x - base);
         part[(a.v0 / kBM + at.m) * a.npad + n] = make_float2(mx, s);
     }
@@ -297,56 +319,60 @@ struct Stage {
 // P of the piece (planes): P[n][v], zeros for tokens past the list and columns past the piece, so
 // that it can serve as depth up to the next multiple of 64.
 template <int BN, bool kMany>
-__global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_probs(Logits a,
+__global__ __launch_bounds__(kTileThreads, 2) void k_ce_probs(Logits a,
                                                                                 const float *__restrict__ lse,
                                                                                 const int32_t *__restrict__ rows,
                                                                                 uint16_t *__restrict__ P, int64_t ldp,
                                                                                 int64_t planep)
 {
-    using T = Tile<false, false, kBM, BN, Waves<BN>::kM, Waves<BN>::kN>;
-    using S = Stage<16 * T::FM, 16 * T::FN, uint16_t>;
-    constexpr int kLds = T::kLds > kTileWaves * S::kBytes ? T::kLds : kTileWaves * S::kBytes;
-    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    using T = Tile<false, false, kBM, BN, kWavesM<BN>, kWavesN<BN>>;
+    using S = Stage<16 * T::FM, 16, uint16_t>;
+    static_assert(kTileWaves * kPlanes * S::kBytes <= T::kLds, "the staged rows fit the tile's LDS");
+    __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
     T tile;
     TilePlace at;
     if (!logits_tile<BN, kMany>(a, tile, at, smem)) return;
     const int l = threadIdx.x & 63, g = l >> 4, wm = T::wave_m(), wn = T::wave_n();
     const int64_t cnt = a.count[0], vw = at.m * kBM + wm * (16 * T::FM), nw = at.n * BN + wn * (16 * T::FN);
-    const bool edge = at.m * kBM + kBM > a.nv;
+    const int valid = (int)(a.nv - vw < 16 * T::FM ? a.nv - vw : 16 * T::FM) - 4 * g;  // rows from the lane's first on
+    const bool edge = a.nv - vw < 16 * T::FM || nw + 16 * T::FN > cnt;
+    constexpr int kOut = kMany ? kPlanes : 1;
+    char *mine = smem + (threadIdx.x >> 6) * (kOut * S::kBytes);
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j) {
+    for (int j = 0; j < T::FN; ++j) {  // 16 tokens at a time
         const int64_t n = nw + j * 16 + (l & 15);
         const bool on = n < cnt;
-        const int64_t t = on ? a.tgt[n] - a.v0 - vw - 4 * g : -1;
-        const float ls = on ? lse[rows[n]] : 0.0f;
+        const int64_t t64 = on ? a.tgt[n] - a.v0 - vw - 4 * g : -1;
+        const int t = t64 >= 0 && t64 < 16 * T::FM && (t64 & 12) == 0 ? (int)t64 : -1;
+        const bool target = __ballot(t >= 0) != 0;  // few waves hold one
+        const float ls = on ? lse[rows[n]] * kLog2e : 0.0f;
+        const int end = on ? valid : 0;
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i)
+        for (int i = 0; i < T::FM; ++i) {
+            float x[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float p = exp_of(tile.acc[i][j][r] - ls) - (t == 16 * i + r ? 1.0f : 0.0f);
-                if (!on || (edge && vw + 16 * i + 4 * g + r >= a.nv)) p = 0.0f;
-                tile.acc[i][j][r] = p;
+            for (int r = 0; r < 4; ++r) x[r] = exp_less(tile.acc[i][j][r], ls);
+            if (target)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] -= t == 16 * i + r ? 1.0f : 0.0f;
+            if (edge)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = 16 * i + r < end ? x[r] : 0.0f;
+            uint32_t b[2][kPlanes];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (kMany) split_pair(x[2 * h], x[2 * h + 1], b[h]);
+                else b[h][0] = pack_bf16(x[2 * h], x[2 * h + 1]);
             }
-    }
-    char *mine = smem + (threadIdx.x >> 6) * S::kBytes;
 #pragma unroll
-    for (int pl = 0; pl < (kMany ? kPlanes : 1); ++pl) {
-#pragma unroll
-        for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-            for (int i = 0; i < T::FM; ++i) {
-                uint16_t b[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float x = tile.acc[i][j][r];
-                    b[r] = kMany ? take_plane(x) : BF16::from_f(x);
-                    tile.acc[i][j][r] = x;
-                }
-                *(uint2 *)(mine + (j * 16 + (l & 15)) * S::kStride + (16 * i + 4 * g) * 2) =
-                    make_uint2((uint32_t)b[0] | (uint32_t)b[1] << 16, (uint32_t)b[2] | (uint32_t)b[3] << 16);
-            }
+            for (int pl = 0; pl < kOut; ++pl)
+                *(uint2 *)(mine + pl * S::kBytes + (l & 15) * S::kStride + (16 * i + 4 * g) * 2) =
+                    make_uint2(b[0][pl], b[1][pl]);
+        }
         wait_lds();
-        S::store(mine, P + pl * planep + nw * ldp + vw, ldp, S::kBytes / S::kStride, 16 * T::FM);
+#pragma unroll
+        for (int pl = 0; pl < kOut; ++pl)
+            S::store(mine + pl * S::kBytes, P + pl * planep + (nw + j * 16) * ldp + vw, ldp, 16, 16 * T::FM);
         wait_lds();
     }
 }
@@ -362,9 +388,9 @@ struct InputGrad {
     int add;
 };
 template <int BN, bool kMany>
-__global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_dx(InputGrad a)
+__global__ __launch_bounds__(kTileThreads, 2) void k_ce_dx(InputGrad a)
 {
-    using T = Tile<true, false, kBM, BN, Waves<BN>::kM, Waves<BN>::kN>;
+    using T = Tile<true, false, kBM, BN, kWavesM<BN>, kWavesN<BN>>;
     __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
     const int64_t cnt = a.count[0];
     const TilePlace at = tile_place(ceil_div(a.D, kBM), ceil_div(cnt, BN), a.splits);
@@ -390,26 +416,6 @@ __global__ __launch_bounds__(kTileThreads, Waves<BN>::kPerSimd) void k_ce_dx(Inp
     }
 }
 
-// dX[n] = the splits' sums of its place in the list, scaled and rounded; zeros if it has none.
-template <typename E>
-__global__ __launch_bounds__(kCeThreads) void k_ce_dx_out(const float *__restrict__ acc, int64_t lda, int64_t plane,
-                                                          int64_t splits, const int32_t *__restrict__ slot, int64_t D,
-                                                          const float *__restrict__ dmean,
-                                                          const float *__restrict__ total,
-                                                          typename E::T *__restrict__ dX)
-{
-    const int64_t n = blockIdx.x, m = slot[n];
-    const float g = grad_scale(dmean, total);
-    for (int64_t c = threadIdx.x; c < D; c += kCeThreads) {
-        float s = 0.0f;
-        if (m >= 0) {
-            for (int64_t k = 0; k < splits; ++k) s += acc[k * plane + m * lda + c];
-            s *= g;
-        }
-        dX[n * D + c] = E::from_f(s);
-    }
-}
-
 struct WeightGrad {
     const uint16_t *P, *X;
     int64_t ldp, ldx, planep, planex;
@@ -420,7 +426,7 @@ struct WeightGrad {
 template <typename E>
 __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typename E::T *__restrict__ dW)
 {
-    using T = Tile<true, true, kBM, 256, 2, 4>;
+    using T = Tile<true, true, kBM, 256, kWavesM<256>, kWavesN<256>>;
     constexpr int kPass = sizeof(typename E::T) == 4 ? 2 : 1;  // fp32 rows leave in two passes
     using S = Stage<16 * T::FM, 16 * T::FN / kPass, typename E::T>;
     constexpr int kLds = T::kLds > kTileWaves * S::kBytes ? T::kLds : kTileWaves * S::kBytes;
@@ -448,8 +454,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typenam
                 if constexpr (kPass == 2) {
                     *(f32x4 *)p = f32x4{v[0] * s, v[1] * s, v[2] * s, v[3] * s};
                 } else {
-                    *(uint2 *)p = make_uint2((uint32_t)BF16::from_f(v[0] * s) | (uint32_t)BF16::from_f(v[1] * s) << 16,
-                                             (uint32_t)BF16::from_f(v[2] * s) | (uint32_t)BF16::from_f(v[3] * s) << 16);
+                    *(uint2 *)p = make_uint2(pack_bf16(v[0] * s, v[1] * s), pack_bf16(v[2] * s, v[3] * s));
                 }
             }
         }
@@ -484,7 +489,7 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
     const int64_t planes = dtype == CSP_F32 ? kPlanes : 1;
     p.npad = round_up(N > 0 ? N : 1, kPad);
     p.ldx = round_up(D, kDepth);
-    p.bn = N <= 64 ? 64 : N <= 128 ? 128 : 256;
+    p.bn = N <= 128 ? 128 : 256;
     p.copy = dtype == CSP_F32 || D % kDepth != 0 || !w_aligned;
     p.tiles = ceil_div(V, kBM);
     p.piece = round_up(V, kPad);
@@ -506,11 +511,21 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         p.zt = take(4 * p.npad);
     } else {
         p.P = take(planes * 2 * p.npad * p.piece);
-        // the depth of dX is cut until its tiles fill the card about twice
+        // The depth of dX is cut so that the rounds of 256 tiles (one a CU) are full: the number of cuts with
+        // the least time, counting 1% for each cut's sums, within 8 steps of depth a cut and 512 MiB of sums.
         const int64_t tiles = ceil_div(D, kBM) * ceil_div(p.npad, p.bn);
-        const int64_t most = ceil_div(p.piece, 8 * kDepth);
-        p.splits = ceil_div(512, tiles);
-        if (p.splits > most) p.splits = most;
+        int64_t most = ceil_div(p.piece, 8 * kDepth), room = ((int64_t)512 << 20) / (4 * p.npad * p.ldx);
+        if (most > room) most = room;
+        if (most > 64) most = 64;
+        p.splits = 1;
+        double best = 1e30;
+        for (int64_t k = 1; k <= most; ++k) {
+            const double t = (double)ceil_div(tiles * k, 256) / (double)k * (1.0 + 0.01 * (double)k);
+            if (t < best) {
+                best = t;
+                p.splits = k;
+            }
+        }
         p.acc = take(4 * p.splits * p.npad * p.ldx);
     }
     p.total = at;
@@ -585,8 +600,7 @@ csp_status fwd_impl(const void *X, const void *W, const int64_t *targets, int64_
         st = ce_piece<E>(p, W, V, D, v0, w, &a, s);
         if (st != CSP_OK) return st;
         const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
-        if (p.bn == 64) k_ce_stats<64, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
-        else if (p.bn == 128) k_ce_stats<128, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
+        if (p.bn == 128) k_ce_stats<128, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
         else k_ce_stats<256, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
         CSP_LAUNCHED("k_ce_stats");
     }
@@ -619,15 +633,13 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
         if (st != CSP_OK) return st;
         if (N > 0) {
             const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
-            if (p.bn == 64) k_ce_probs<64, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
-            else if (p.bn == 128) k_ce_probs<128, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
+            if (p.bn == 128) k_ce_probs<128, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
             else k_ce_probs<256, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
             CSP_LAUNCHED("k_ce_probs");
             const InputGrad d{P, a.W, p.piece, a.ldw, planep, a.planew, count, a.nv, D, p.splits, per,
                               (float *)(w + p.acc), p.ldx, p.npad * p.ldx, v0 > 0};
             const unsigned gx = (unsigned)(ceil_div(D, kBM) * ceil_div(N, p.bn) * p.splits);
-            if (p.bn == 64) k_ce_dx<64, kMany><<<gx, kTileThreads, 0, s>>>(d);
-            else if (p.bn == 128) k_ce_dx<128, kMany><<<gx, kTileThreads, 0, s>>>(d);
+            if (p.bn == 128) k_ce_dx<128, kMany><<<gx, kTileThreads, 0, s>>>(d);
             else k_ce_dx<256, kMany><<<gx, kTileThreads, 0, s>>>(d);
             CSP_LAUNCHED("k_ce_dx");
         }
@@ -636,9 +648,9 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
         CSP_LAUNCHED("k_ce_dw");
     }
     if (N > 0) {
-        k_ce_dx_out<E><<<(unsigned)N, kCeThreads, 0, s>>>((const float *)(w + p.acc), p.ldx, p.npad * p.ldx, p.splits,
-                                                          (const int32_t *)(w + p.slot), D, dmean, total, (T *)dX);
-        CSP_LAUNCHED("k_ce_dx_out");
+        k_ce_out<E><<<out_blocks(N, D), 256, 0, s>>>((const float *)(w + p.acc), p.ldx, p.npad * p.ldx, (int)p.splits,
+                                                     (const int32_t *)(w + p.slot), N, D, dmean, total, (T *)dX);
+        CSP_LAUNCHED("k_ce_out");
     }
     return CSP_OK;
 }

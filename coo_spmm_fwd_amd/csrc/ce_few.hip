@@ -11,7 +11,7 @@
 //   forward   k_few_prep, k_few_rows (logits -> maximum and sum of each 128
 //             vocabulary rows), k_few_join
 //   backward  k_few_prep, k_few_rows (logits -> P -> dW rows, and P for dX),
-//             k_few_dx, k_few_out
+//             k_few_dx, k_ce_out
 //
 // A wave holds 32 vocabulary rows.  Its logits come out with a vocabulary row
 // a lane (lane % 16) and tokens 4 (lane / 16) + r in the registers, which is
@@ -27,9 +27,7 @@
 namespace csp {
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFewThreads = 256, kFewWaves = 4;
@@ -56,25 +54,6 @@ template <typename E> __host__ __device__ constexpr int depth_of(int q, int j)
 template <typename E> __host__ __device__ constexpr int column_of(int f, int m)
 {
     return Form<E>::kPlanes == 1 ? 32 * (f >> 1) + 8 * (m >> 2) + 4 * (f & 1) + (m & 3) : 16 * f + m;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)  // round to nearest even
-{
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
-__device__ __forceinline__ float low_of(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float high_of(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
-
-// Two floats as three pairs of bf16, x = x0 + x1 + x2: each the rest rounded to nearest.  Values past the
-// largest bf16 leave the excess to the second plane.  An infinity ends as NaN (infinity less infinity).
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[3])
-{
-    constexpr float kMax = 3.38953139e38f;
-    p[0] = pack_bf16(__builtin_amdgcn_fmed3f(a, -kMax, kMax), __builtin_amdgcn_fmed3f(b, -kMax, kMax));
-    a -= low_of(p[0]);
-    b -= high_of(p[0]);
-    p[1] = pack_bf16(a, b);
-    p[2] = pack_bf16(a - low_of(p[1]), b - high_of(p[1]));
 }
 
 template <typename E> struct Frag {
@@ -664,35 +643,6 @@ __global__ __launch_bounds__(kFewThreads, NB == 4 ? 1 : 2) void k_few_dx(FewDx a
     }
 }
 
-// dX[n] = the splits' sums of its place in the list, scaled and rounded; zeros if it has none.
-template <typename E>
-__global__ __launch_bounds__(kFewThreads) void k_few_out(const float *__restrict__ acc, int64_t lda, int64_t plane,
-                                                         int splits, const int32_t *__restrict__ slot, int N, int64_t D,
-                                                         const float *__restrict__ dmean,
-                                                         const float *__restrict__ total,
-                                                         typename E::T *__restrict__ dX)
-{
-    const int64_t groups = (D + 3) / 4, i = (int64_t)blockIdx.x * kFewThreads + threadIdx.x;
-    const int64_t n = i / groups, c = (i - n * groups) * 4;
-    if (n >= N) return;
-    const int m = slot[n];
-    const float scale = grad_scale(dmean, total);
-    f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
-    if (m >= 0) {
-        const float *p = acc + m * lda + c;
-        constexpr int kAhead = 8;
-        for (int k = 0; k < splits; k += kAhead) {  // splits are a multiple of 8
-            f32x4 x[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) x[j] = *(const f32x4 *)(p + (k + j) * plane);
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) s += x[j];
-        }
-        s *= scale;
-    }
-    for (int k = 0; k < 4 && c + k < D; ++k) dX[n * D + c + k] = E::from_f(s[k]);
-}
-
 struct FewPlan {
     int nb, splits, per;
     int64_t steps, frags, tiles, lda;  // depth steps of 32 of Xf, fragments of Xt, workgroups of 128 rows
@@ -806,9 +756,9 @@ csp_status bwd_few(const void *X, const void *W, const int64_t *targets, int64_t
     const FewDx d{a.Pf, V, D, p.splits, p.per, (float *)(w + p.acc), p.lda, 16 * NB * p.lda};
     k_few_dx<E, NB><<<(unsigned)(p.splits * ceil_div(D, kDxCols<E>)), kFewThreads, 0, s>>>(d, (const T *)W);
     CSP_LAUNCHED("k_few_dx");
-    k_few_out<E><<<(unsigned)ceil_div(N * ceil_div(D, 4), kFewThreads), kFewThreads, 0, s>>>(
-        d.acc, p.lda, d.plane, p.splits, (const int32_t *)(w + p.slot), (int)N, D, dmean, total, (T *)dX);
-    CSP_LAUNCHED("k_few_out");
+    k_ce_out<E><<<out_blocks(N, D), 256, 0, s>>>(d.acc, p.lda, d.plane, p.splits, (const int32_t *)(w + p.slot), N, D,
+                                                 dmean, total, (T *)dX);
+    CSP_LAUNCHED("k_ce_out");
     return CSP_OK;
 }
 

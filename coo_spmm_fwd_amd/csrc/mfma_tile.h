@@ -8,19 +8,31 @@
 // LDS by 16-byte loads that bypass the registers, and the second is turned on
 // its way out of LDS by the transposing 64-bit read.
 //
-// Depth is walked in steps of 64 with two LDS buffers and, inside a step, two
-// register sets of 32: while the matrix units work on one half, the next half
-// (of the same step, or of the following one) is read from LDS.  One barrier
-// a step: it comes between the halves, when every wave has read its second
-// half (so the buffer is free for step + 2) and its own loads of step + 1
-// have landed.
+// Depth is walked in steps of 32 through a ring of 5 LDS slots and two register
+// sets: while the matrix units work on step h, step h + 1 is read from LDS into
+// the other registers, steps h + 2 to h + 4 are on their way, and the loads of
+// step h + 5 go into the slot that step h was read from.  One barrier a step:
+// every wave has read step h + 1, and its own loads of step h + 2 have landed.
+// A load so has three to four steps, of 1024 cycles of the matrix units each,
+// to arrive.
+//
+// 8 waves, two a SIMD: while one issues reads, loads or its epilogue, the other
+// feeds the matrix unit (4 waves of 128 x 128 read less from LDS, but LDS is
+// not the bound, and every instruction between their products is a gap).  Reads
+// and loads are issued between blocks of products, a few at a time.  The
+// products are written as asm with their sums tied in place: left to itself
+// the compiler moves sums from register to register in the loop.  What it would
+// do for them is done by hand: two wait states before a block (operands may
+// come from a move), and 16 after a pair of steps (a loop may end there).
 //
 // fp32 operands are held as three bf16 planes, x = x0 + x1 + x2 with each
 // plane the rest rounded to nearest, 24 bits in all.  Six of the nine plane
 // products are taken; the three left out are below 2^-25 of |x w|, under the
-// rounding of the fp32 sum itself.  They are walked as six steps of depth in
+// rounding of the fp32 sum itself.  They are walked as six pairs of steps in
 // place of one.
 #pragma once
+
+#include <type_traits>
 
 #include "common.h"
 #include "device_util.h"
@@ -32,7 +44,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kDepth = 64;        // k of a step
+constexpr int kDepth = 64;        // k of a pair of steps
+constexpr int kStep = 32;         // k of a step
+constexpr int kSlots = 5;
 constexpr int kTileWaves = 8;
 constexpr int kTileThreads = 64 * kTileWaves;
 constexpr int kPlanes = 3;        // planes of an fp32 operand
@@ -58,10 +72,11 @@ __device__ __forceinline__ void load_to_lds(const uint16_t *base, uint32_t off, 
                  : "memory");  // m0 is the compiler's only for instructions that none of these kernels has
 }
 // Waits as builtins: the compiler counts them, and adds none of its own for what they cover.
+template <int kLeft = 0>  // all but the last kLeft loads
 __device__ __forceinline__ void wait_loads()
 {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (kLeft & 15) | (kLeft >> 4) << 14);
     asm volatile("" ::: "memory");
 }
 __device__ __forceinline__ void wait_lds()
@@ -91,20 +106,29 @@ typedef __attribute__((address_space(3))) char lds_char;
 // blocks of 16 that start at block wb.
 template <bool kDepthMajor, int BR, int FR>
 struct TileSide {
-    static constexpr int kLoads = BR / 64;             // 1 KiB loads a wave and step
-    static constexpr int kBytes = BR * kDepth * 2;     // one buffer
-    static constexpr int kGroups = BR / 8;             // 16-byte groups of a depth row (kDepthMajor)
-    static constexpr int kAddrs = kDepthMajor ? FR : 2;
+    static constexpr int kLoads = BR * kStep * 2 / 1024 / kTileWaves;  // 1 KiB loads a wave and step
+    static constexpr int kBytes = BR * kStep * 2;                      // one slot
+    static constexpr int kGroups = BR / 8;                             // 16-byte groups of a depth row (kDepthMajor)
+    static constexpr int kAddrs = kDepthMajor ? FR : 1;
+    static constexpr int kKinds = kDepthMajor ? 2 : 1;
 
-    uint32_t off[kLoads];
+    uint32_t off[kKinds][kLoads];  // kDepthMajor: of even and odd steps (they differ in a last part)
     uint32_t addr[kAddrs];
 
-    // LDS image, rows with k along them: 128 bytes a row, its 16-byte group c
-    // at c ^ (row & 7), so that the 8 rows a read touches at once lie in
+    // LDS image, rows with k along them: 64 bytes a row, its 16-byte group c
+    // at c ^ (row / 2 & 3), so that the 8 rows a read touches at once lie in
     // different banks.  Depth rows: 2 BR bytes each, 32-byte pairs of groups
     // at pair ^ f(k), f = 2 low bits of k and bit 3: the rows that one
     // transposing read touches at once.
     __device__ static int fold(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+
+    // Offset of load j of a depth-major step, depth rows from `left` on repeating the one before.
+    __device__ static uint32_t depth_off(const TileOperand &o, int j, int left)
+    {
+        const int e = ((int)(threadIdx.x >> 6) + kTileWaves * j) * 64 + (int)(threadIdx.x & 63), k = e / kGroups;
+        const int q = (e % kGroups) ^ (fold(k) << 1);
+        return (uint32_t)min(k, left - 1) * (uint32_t)(2 * o.ld) + (uint32_t)min(q, o.rows / 8 - 1) * 16u;
+    }
 
     __device__ void setup(const TileOperand &o, int wb, uint32_t lds)
     {
@@ -112,63 +136,67 @@ struct TileSide {
         if constexpr (!kDepthMajor) {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
-                const int r = (w + kTileWaves * j) * 8 + (l >> 3);
-                off[j] = (uint32_t)(min(r, o.rows - 1)) * (uint32_t)(2 * o.ld) + (uint32_t)(((l & 7) ^ (l >> 3)) * 16);
+                const int r = (w + kTileWaves * j) * 16 + (l >> 2);
+                off[0][j] = (uint32_t)(min(r, o.rows - 1)) * (uint32_t)(2 * o.ld) + (uint32_t)(((l & 3) ^ (r >> 1 & 3)) * 16);
             }
             const int r = wb * 16 + (l & 15);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) addr[h] = lds + r * 128 + (((l >> 4) + 4 * h) ^ (l & 7)) * 16;
+            addr[0] = lds + r * 64 + ((l >> 4) ^ (r >> 1 & 3)) * 16;
         } else {
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int e = (w + kTileWaves * j) * 64 + l, k = e / kGroups;
-                const int q = (e % kGroups) ^ (fold(k) << 1);
-                off[j] = (uint32_t)k * (uint32_t)(2 * o.ld) + (uint32_t)min(q, o.rows / 8 - 1) * 16u;
-            }
+            clamp<0>(o, kStep);
+            clamp<1>(o, kStep);
             const int i = l & 15, k = 8 * (l >> 4) + (i >> 2);
 #pragma unroll
             for (int b = 0; b < FR; ++b) addr[b] = lds + k * (2 * BR) + ((wb + b) ^ fold(k)) * 32 + 8 * (i & 3);
         }
     }
-
-    // Issues the loads of one step; `left` = depth rows from the step's first to the end (kDepthMajor).
-    __device__ void load(const TileOperand &o, int64_t at, int64_t left, uint32_t lds)
+    template <int kKind>
+    __device__ void clamp(const TileOperand &o, int left)
     {
-        const uint16_t *p = uniform_ptr(o.base + at);
-        const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            uint32_t f = off[j];
-            if constexpr (kDepthMajor) {
-                if (left < kDepth) {  // the last step of a depth that is no multiple of 64
-                    const int l = threadIdx.x & 63, e = (w + kTileWaves * j) * 64 + l, k = e / kGroups;
-                    const int q = (e % kGroups) ^ (fold(k) << 1);
-                    f = (uint32_t)min(k, (int)left - 1) * (uint32_t)(2 * o.ld) + (uint32_t)min(q, o.rows / 8 - 1) * 16u;
-                }
-            }
-            load_to_lds(p, f, lds + (w + kTileWaves * j) * 1024);
-        }
+        for (int j = 0; j < kLoads; ++j) off[kKind][j] = depth_off(o, j, left);
     }
 
-    // The FR blocks of half h from the buffer at byte `buf` past the first.
-    template <int kHalf, int kBuf>
-    __device__ void read(bf16x8 (&frag)[FR])
+    // Load j of an even or odd step, from p (uniform) into the slot at lds.
+    template <int kKind>
+    __device__ void load(const uint16_t *p, int j, uint32_t lds)
+    {
+        load_to_lds(p, off[kKinds == 2 ? kKind : 0][j], lds + (uint32_t)j * (kTileWaves * 1024));
+    }
+
+    // Moves the reads to another slot.
+    __device__ void turn(int bytes)
     {
 #pragma unroll
-        for (int b = 0; b < FR; ++b) {
-            if constexpr (!kDepthMajor) {
-                frag[b] = *(const __attribute__((address_space(3))) bf16x8 *)(uintptr_t)(addr[kHalf] + kBuf * kBytes + b * 2048);
-            } else {
-                const uint32_t a = addr[b] + kBuf * kBytes + kHalf * 32 * (2 * BR);
-                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)a);
-                const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(a + 4 * (2 * BR)));
-                const s16x8 z = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-                frag[b] = __builtin_bit_cast(bf16x8, z);
-            }
+        for (int i = 0; i < kAddrs; ++i) addr[i] += (uint32_t)bytes;
+    }
+
+    // Block b from the current slot.
+    __device__ bf16x8 read(int b)
+    {
+        if constexpr (!kDepthMajor) {
+            return *(const __attribute__((address_space(3))) bf16x8 *)(uintptr_t)(addr[0] + b * 1024);
+        } else {
+            const uint32_t a = addr[b];
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)a);
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4 *)(uintptr_t)(a + 4 * (2 * BR)));
+            const s16x8 z = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+            return __builtin_bit_cast(bf16x8, z);
         }
     }
 };
+
+// c[j] += a b[j] of 16 x 16 x 32.
+__device__ __forceinline__ void products(f32x4 (&c)[4], bf16x8 a, const bf16x8 (&b)[4])
+{
+    asm volatile("s_nop 1\n\t"
+                 "v_mfma_f32_16x16x32_bf16 %0, %4, %5, %0\n\t"
+                 "v_mfma_f32_16x16x32_bf16 %1, %4, %6, %1\n\t"
+                 "v_mfma_f32_16x16x32_bf16 %2, %4, %7, %2\n\t"
+                 "v_mfma_f32_16x16x32_bf16 %3, %4, %8, %3"
+                 : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3])
+                 : "v"(a), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]));
+}
 
 // Wave (wm, wn) of kWM x kWN holds rows m = (wm FM + i) 16 + 4 (lane / 16) + r
 // and columns n = (wn FN + j) 16 + lane % 16 in acc[i][j][r].
@@ -178,28 +206,41 @@ struct Tile {
     static constexpr int FM = BM / kWM / 16, FN = BN / kWN / 16;
     using SideA = TileSide<kADepth, BM, FM>;
     using SideB = TileSide<kBDepth, BN, FN>;
-    static constexpr int kLds = 2 * (SideA::kBytes + SideB::kBytes);
+    static constexpr int kLds = kSlots * (SideA::kBytes + SideB::kBytes);
 
     f32x4 acc[FM][FN];
 
-    __device__ static int wave_m() { return (threadIdx.x >> 6) / kWN; }
-    __device__ static int wave_n() { return (threadIdx.x >> 6) % kWN; }
+    __device__ static int wave_m() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWN; }
+    __device__ static int wave_n() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWN; }
 
-    __device__ __forceinline__ void multiply(const bf16x8 (&a)[FM], const bf16x8 (&b)[FN])
+    // Products of one step, and between their blocks the reads of the next into (an, bn), early enough to be
+    // there at the end, and other(i).
+    template <typename Other>
+    __device__ __forceinline__ void step(SideA &sa, SideB &sb, const bf16x8 (&a)[FM], const bf16x8 (&b)[FN],
+                                         bf16x8 (&an)[FM], bf16x8 (&bn)[FN], Other &&other)
     {
+        constexpr int kEach = (FM + FN + FM - 3) / (FM - 2);  // all reads under all blocks but two
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int i = 0; i < FM; ++i) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+            for (int r = i * kEach; r < (i + 1) * kEach && r < FM + FN; ++r) {
+                if (r < FN) bn[r] = sb.read(r);
+                else an[r - FN] = sa.read(r - FN);
+            }
+            other(i);
+            __builtin_amdgcn_sched_barrier(0);
+            products(acc[i], a[i], b);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 
     // depth: valid k (operands with k along their rows are readable, and zero on one side, up to a
-    // multiple of 64); planes: 1, or kPlanes for fp32 operands.
+    // multiple of 64); planes: whether the operands are fp32 in planes.
     __device__ __forceinline__ void run(const TileOperand &A, const TileOperand &B, int64_t depth, bool planes,
                                         char *smem)
     {
         const uint32_t lds = (uint32_t)(uintptr_t)(lds_char *)smem;
-        const uint32_t la = lds, lb = lds + 2 * SideA::kBytes;
+        const uint32_t la = lds, lb = lds + kSlots * SideA::kBytes;
         SideA sa;
         SideB sb;
         sa.setup(A, wave_m() * FM, la);
@@ -208,53 +249,102 @@ struct Tile {
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int steps = (int)((depth + kDepth - 1) / kDepth) * (planes ? kPlaneProducts : 1);
+        const int segs = planes ? kPlaneProducts : 1;
+        const int steps = (int)((depth + kDepth - 1) / kDepth) * segs * 2;  // even
         if (steps == 0) return;
+        const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
         int64_t k0 = 0;
-        int seg = 0;
-        auto load = [&](int buf) {  // the next step into buffer buf
-            const int pa = planes ? 0x850 >> (2 * seg) & 3 : 0, pb = planes ? 0x244 >> (2 * seg) & 3 : 0;
-            sa.load(A, pa * A.plane + (kADepth ? k0 * A.ld : k0), depth - k0, la + buf * SideA::kBytes);
-            sb.load(B, pb * B.plane + (kBDepth ? k0 * B.ld : k0), depth - k0, lb + buf * SideB::kBytes);
-            if (!planes || ++seg == kPlaneProducts) {
-                seg = 0;
-                k0 += kDepth;
+        int seg = 0, made = 0, slot = 0;
+        const uint16_t *pa, *pb;
+        // Where the operands of the next step begin, an even or odd one; steps past the end repeat the last
+        // two.  No branch: the loops below are single blocks, in which the sums keep their registers.
+        auto next = [&](auto odd) {
+            constexpr int kOdd = decltype(odd)::value;
+            const int qa = planes ? 0x850 >> (2 * seg) & 3 : 0, qb = planes ? 0x244 >> (2 * seg) & 3 : 0;
+            const int64_t k = k0 + kOdd * kStep, kd = k < depth ? k : depth - 1;
+            pa = uniform_ptr(A.base + qa * A.plane + (kADepth ? kd * A.ld : k));
+            pb = uniform_ptr(B.base + qb * B.plane + (kBDepth ? kd * B.ld : k));
+            if constexpr (kOdd) {
+                made += 2;
+                const bool wrap = seg + 1 == segs, more = made < steps;
+                seg = more ? (wrap ? 0 : seg + 1) : seg;
+                k0 += more && wrap ? kDepth : 0;
             }
         };
+        // load i of that step into the free slot
+        constexpr int kAll = SideA::kLoads + SideB::kLoads;
+        static_assert(kAll <= FM, "a load for each block of products");
+        auto load = [&](auto odd, int i) {
+            constexpr int kOdd = decltype(odd)::value;
+            if (i < SideA::kLoads) sa.template load<kOdd>(pa, i, la + wave + slot * SideA::kBytes);
+            else if (i < kAll) sb.template load<kOdd>(pb, i - SideA::kLoads, lb + wave + slot * SideB::kBytes);
+        };
+        // Loads from the last part of a depth that is no multiple of 64: steps from `tail` on.
+        const int tail = steps - 2 * segs, left = (int)(depth - (depth - 1) / kDepth * kDepth);
+        auto clamp = [&](auto odd) {
+            constexpr int kOdd = decltype(odd)::value;
+            if (left == kDepth) return;
+            const int part = kOdd ? (left > kStep ? left - kStep : 1) : left;
+            if constexpr (kADepth) sa.template clamp<kOdd>(A, part);
+            if constexpr (kBDepth) sb.template clamp<kOdd>(B, part);
+        };
+        const std::integral_constant<int, 0> even;
+        const std::integral_constant<int, 1> odd;
+        auto first = [&](int h, auto kind) {
+            if (h == tail || (h == 0 && tail < 0)) clamp(even);
+            if (h == tail + 1) clamp(odd);
+            next(kind);
+#pragma unroll
+            for (int i = 0; i < kAll; ++i) load(kind, i);
+            slot = slot + 1 == kSlots ? 0 : slot + 1;
+        };
+        first(0, even);
+        first(1, odd);
+        first(2, even);
+        first(3, odd);
+        first(4, even);
         bf16x8 a0[FM], b0[FN], a1[FM], b1[FN];
-        load(0);
-        wait_loads();
+        wait_loads<3 * kAll>();
         tile_barrier();
-        if (steps > 1) load(1);
-        sa.template read<0, 0>(a0);
-        sb.template read<0, 0>(b0);
-        for (int t = 0; t < steps; t += 2) {
-            step<0>(sa, sb, a0, b0, a1, b1, t, steps, load);
-            if (t + 1 < steps) step<1>(sa, sb, a0, b0, a1, b1, t + 1, steps, load);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) a0[i] = sa.read(i);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b0[j] = sb.read(j);
+        wait_lds();
+        tile_barrier();
+        auto turn = [&]() {  // the reads move to slot + 1, then the loads too
+            sa.turn(slot + 1 == kSlots ? -(kSlots - 1) * SideA::kBytes : SideA::kBytes);
+            sb.turn(slot + 1 == kSlots ? -(kSlots - 1) * SideB::kBytes : SideB::kBytes);
+        };
+        auto pair = [&]() {
+            turn();
+            next(odd);
+            step(sa, sb, a0, b0, a1, b1, [&](int i) { load(odd, i); });
+            wait_lds();
+            wait_loads<3 * kAll>();
+            tile_barrier();
+            slot = slot + 1 == kSlots ? 0 : slot + 1;
+            turn();
+            next(even);
+            step(sa, sb, a1, b1, a0, b0, [&](int i) { load(even, i); });
+            asm volatile("s_nop 15");  // the sums are written before anything that follows a loop moves them
+            wait_lds();
+            wait_loads<3 * kAll>();
+            tile_barrier();
+            slot = slot + 1 == kSlots ? 0 : slot + 1;
+        };
+        int h = 0;
+        for (; h + 6 < tail; h += 2) pair();
+        if (tail > 4) clamp(even);
+        if (h < steps && h + 5 < tail) {
+            pair();
+                h += 2;
         }
-        wait_lds();
-        tile_barrier();  // LDS is the caller's now
-    }
-
-    template <int kBuf, typename Load>
-    __device__ __forceinline__ void step(SideA &sa, SideB &sb, bf16x8 (&a0)[FM], bf16x8 (&b0)[FN], bf16x8 (&a1)[FM],
-                                         bf16x8 (&b1)[FN], int t, int steps, Load &load)
-    {
-        sa.template read<1, kBuf>(a1);
-        sb.template read<1, kBuf>(b1);
-        __builtin_amdgcn_sched_barrier(0);  // reads first: the products below wait for none of them
-        multiply(a0, b0);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_lds();
+        if (tail + 1 > 4) clamp(odd);
+        for (; h < steps; h += 2) pair();
         wait_loads();
-        tile_barrier();
-        if (t + 2 < steps) load(kBuf);
-        // after the last step: the buffer of the step before, read and not used
-        sa.template read<0, 1 - kBuf>(a0);
-        sb.template read<0, 1 - kBuf>(b0);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(a1, b1);
-        __builtin_amdgcn_sched_barrier(0);
+        wait_lds();
+        tile_barrier();  // LDS is the caller's now (the loads that nothing uses have landed)
     }
 };
 

@@ -1,0 +1,68 @@
+"""The two ends of a language model's training step as torch functions: embedding, linear cross
+entropy and gradient clipping (the library's embed_*, linear_ce_* and grad_* calls).
+
+    Y = embedding(ids, E, scale)              # rows of E, differentiable in E
+    loss = linear_cross_entropy(X, W, t)      # mean over targets inside [0, V), differentiable in X and W
+    norm = clip_grad_norm(params, max_norm)   # scales .grad in place, returns the norm before
+
+ids and targets outside [0, V) take no part: padding rows are zero and masked tokens (-100, say)
+cost nothing and get zero gradients.  Nothing here reads back to the host, so a step made of these
+can be captured in a HIP graph; as with any autograd capture, drop the losses and gradients of eager
+steps on the same parameters first (their graph holds the parameters' accumulation nodes on the
+eager stream).
+
+Argument marshalling only: every step runs in the HIP library.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as csp
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, E, ids, scale):
+        ctx.save_for_backward(ids)
+        ctx.vocab, ctx.scale = E.shape[0], scale
+        return csp.embed_fwd(E, ids, scale)
+
+    @staticmethod
+    def backward(ctx, dY):
+        (ids,) = ctx.saved_tensors
+        return csp.embed_bwd(dY.contiguous(), ids, ctx.vocab, ctx.scale), None, None
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, targets):
+        loss, lse, total = csp.linear_ce_fwd(X, W, targets)
+        ctx.save_for_backward(X, W, targets, lse, total)
+        return total[2].clone()  # the backward reads total; the caller may change its loss in place
+
+    @staticmethod
+    def backward(ctx, dmean):
+        X, W, targets, lse, total = ctx.saved_tensors
+        dX, dW = csp.linear_ce_bwd(X, W, targets, lse, dmean.reshape(1).contiguous(), total)
+        return dX, dW, None
+
+
+def embedding(ids, E, scale: float = 1.0):
+    """scale * E[ids] as [*ids.shape, D]; a zero row for an id outside [0, V)."""
+    Y = _Embedding.apply(E, ids.reshape(-1).contiguous(), float(scale))
+    return Y.view(*ids.shape, E.shape[1])
+
+
+def linear_cross_entropy(X, W, targets):
+    """Mean cross entropy of the logits X W^T [..., V] (never stored) against targets [...], as an fp32
+    scalar; the mean is over the targets inside [0, V), and 0 if there are none."""
+    if tuple(X.shape[:-1]) != tuple(targets.shape):
+        raise ValueError(f"X is {tuple(X.shape)} but targets are {tuple(targets.shape)}")
+    return _LinearCrossEntropy.apply(X.reshape(-1, X.shape[-1]).contiguous(), W, targets.reshape(-1).contiguous())
+
+
+@torch.no_grad()
+def clip_grad_norm(params, max_norm: float):
+    """Scale the parameters' gradients in place by min(1, max_norm / (norm + 1e-6)); returns the norm
+    over all of them before that, as an fp32 tensor [1]."""
+    return csp.grad_clip([p.grad for p in params if p.grad is not None], max_norm)

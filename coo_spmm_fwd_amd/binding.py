@@ -135,9 +135,15 @@ def _check(st: int):
 
 
 # ------------------------------------------------------------ marshalling
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream):
@@ -495,95 +501,109 @@ def _work(nbytes: int, device, stream):
     return _new(nbytes, _torch().uint8, device, stream)
 
 
-def _device(*tensors):
-    """All tensors have to be on the current device (its stream is used)."""
-    torch = _torch()
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t.get_device() != here:
-            raise ValueError(f"a tensor is on {t.device}, which is not the current device")
+def _here(t) -> int:
+    """The current device, where all tensors of a call have to be (its stream is used); -1 if t is on none."""
+    return _torch().cuda.current_device() if getattr(t, "is_cuda", False) else -1
 
 
-def _matrix(t, name, dtype=None):
-    """Pointer and shape of a contiguous fp32 or bf16 GPU matrix."""
-    p = _dev(t, name, dtype)
+def _ptr(t, name, here, dtype, shape=None) -> int:
+    """Device address of a contiguous tensor on device `here`."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _matrix(t, name, here, like=None):
+    """Address, shape and dtype code of a contiguous GPU matrix of fp32 or bf16, or of the type of `like`."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a GPU tensor")
+    code = _dtype_code(t)
+    p = _ptr(t, name, here, t.dtype if like is None else like.dtype)
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
-    return p, int(t.shape[0]), int(t.shape[1])
+    rows, cols = t.shape
+    return p, rows, cols, code
 
 
 def embed_fwd(E, ids, scale: float = 1.0, Y=None, stream=None):
     """Y[n, :] = scale * E[ids[n], :]; ids int64 [N], a zero row for an id outside [0, V)."""
-    torch = _torch()
-    ep, V, D = _matrix(E, "E")
-    dt = _dtype_code(E)
-    N = int(ids.numel())
-    ip = _dev(ids, "ids", torch.int64, (N,))
+    here = _here(E)
+    ep, V, D, dt = _matrix(E, "E", here)
+    N = ids.numel()
+    ip = _ptr(ids, "ids", here, _torch().int64, (N,))
     if Y is None:
         Y = _new((N, D), E.dtype, E.device, stream)
-    yp = _dev(Y, "Y", E.dtype, (N, D))
-    _device(E, ids, Y)
-    _check(load().embed_fwd(ep, ip, N, V, D, dt, float(scale), yp, _stream(stream)))
+    else:
+        _ptr(Y, "Y", here, E.dtype, (N, D))
+    _check(load().embed_fwd(ep, ip, N, V, D, dt, float(scale), Y.data_ptr(), _stream(stream)))
     return Y
 
 
 def embed_bwd(dY, ids, V: int, scale: float = 1.0, dE=None, stream=None):
     """dE[v, :] = scale * sum over n with ids[n] = v of dY[n, :], as [V, D] (zero rows where no id is v)."""
-    torch = _torch()
-    gp, N, D = _matrix(dY, "dY")
-    dt = _dtype_code(dY)
+    here = _here(dY)
+    gp, N, D, dt = _matrix(dY, "dY", here)
     V = int(V)
-    ip = _dev(ids, "ids", torch.int64, (N,))
+    ip = _ptr(ids, "ids", here, _torch().int64, (N,))
     L = load()
     w = _work(L.embed_bwd_workspace(N, V, D, dt), dY.device, stream)
     if dE is None:
         dE = _new((V, D), dY.dtype, dY.device, stream)
-    ep = _dev(dE, "dE", dY.dtype, (V, D))
-    _device(dY, ids, dE)
-    _check(L.embed_bwd(gp, ip, N, V, D, dt, float(scale), ep, c_void_p(w.data_ptr()), w.numel(), _stream(stream)))
+    else:
+        _ptr(dE, "dE", here, dY.dtype, (V, D))
+    _check(L.embed_bwd(gp, ip, N, V, D, dt, float(scale), dE.data_ptr(), w.data_ptr(), w.numel(), _stream(stream)))
     return dE
+
+
+def _ce_inputs(X, W, targets):
+    here = _here(X)
+    xp, N, D, dt = _matrix(X, "X", here)
+    wp, V, D2, _ = _matrix(W, "W", here, X)
+    if D2 != D:
+        raise ValueError(f"X is {N} x {D} but W is {V} x {D2}")
+    return here, xp, wp, _ptr(targets, "targets", here, _torch().int64, (N,)), N, V, D, dt
+
+
+def _out(t, name, here, dtype, shape, device, stream):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    _ptr(t, name, here, dtype, shape)
+    return t
 
 
 def linear_ce_fwd(X, W, targets, loss=None, lse=None, total=None, stream=None):
     """Cross entropy of the logits X W^T against int64 targets, the logits not stored: fp32 tensors
     loss [N], lse [N] and total = {sum, count, mean} over the targets inside [0, V)."""
-    torch = _torch()
-    xp, N, D = _matrix(X, "X")
-    wp, V, D2 = _matrix(W, "W", X.dtype)
-    if D2 != D:
-        raise ValueError(f"X is {N} x {D} but W is {V} x {D2}")
-    dt = _dtype_code(X)
-    tp = _dev(targets, "targets", torch.int64, (N,))
-    L = load()
-    w = _work(L.linear_ce_workspace(N, V, D, dt, 0), X.device, stream)
-    loss = _new((N,), torch.float32, X.device, stream) if loss is None else loss
-    lse = _new((N,), torch.float32, X.device, stream) if lse is None else lse
-    total = _new((3,), torch.float32, X.device, stream) if total is None else total
-    op, ep = _dev(loss, "loss", torch.float32, (N,)), _dev(lse, "lse", torch.float32, (N,))
-    sp = _dev(total, "total", torch.float32, (3,))
-    _device(X, W, targets, loss, lse, total)
-    _check(L.linear_ce_fwd(xp, wp, tp, N, V, D, dt, op, ep, sp, c_void_p(w.data_ptr()), w.numel(), _stream(stream)))
+    here, xp, wp, tp, N, V, D, dt = _ce_inputs(X, W, targets)
+    L, dev, f32 = load(), X.device, _torch().float32
+    w = _work(L.linear_ce_workspace(N, V, D, dt, 0), dev, stream)
+    loss = _out(loss, "loss", here, f32, (N,), dev, stream)
+    lse = _out(lse, "lse", here, f32, (N,), dev, stream)
+    total = _out(total, "total", here, f32, (3,), dev, stream)
+    _check(L.linear_ce_fwd(xp, wp, tp, N, V, D, dt, loss.data_ptr(), lse.data_ptr(), total.data_ptr(), w.data_ptr(),
+                           w.numel(), _stream(stream)))
     return loss, lse, total
 
 
 def linear_ce_bwd(X, W, targets, lse, dmean, total, dX=None, dW=None, stream=None):
     """Gradients (dX, dW) of dmean * mean loss; lse and total from linear_ce_fwd, dmean fp32 [1]."""
-    torch = _torch()
-    xp, N, D = _matrix(X, "X")
-    wp, V, D2 = _matrix(W, "W", X.dtype)
-    if D2 != D:
-        raise ValueError(f"X is {N} x {D} but W is {V} x {D2}")
-    dt = _dtype_code(X)
-    tp = _dev(targets, "targets", torch.int64, (N,))
-    ep = _dev(lse, "lse", torch.float32, (N,))
-    gp, sp = _dev(dmean, "dmean", torch.float32, (1,)), _dev(total, "total", torch.float32, (3,))
-    L = load()
-    w = _work(L.linear_ce_workspace(N, V, D, dt, 1), X.device, stream)
-    dX = _new((N, D), X.dtype, X.device, stream) if dX is None else dX
-    dW = _new((V, D), X.dtype, X.device, stream) if dW is None else dW
-    dxp, dwp = _dev(dX, "dX", X.dtype, (N, D)), _dev(dW, "dW", X.dtype, (V, D))
-    _device(X, W, targets, lse, dmean, total, dX, dW)
-    _check(L.linear_ce_bwd(xp, wp, tp, N, V, D, dt, ep, gp, sp, dxp, dwp, c_void_p(w.data_ptr()), w.numel(),
+    here, xp, wp, tp, N, V, D, dt = _ce_inputs(X, W, targets)
+    L, dev, f32 = load(), X.device, _torch().float32
+    ep = _ptr(lse, "lse", here, f32, (N,))
+    gp, sp = _ptr(dmean, "dmean", here, f32, (1,)), _ptr(total, "total", here, f32, (3,))
+    w = _work(L.linear_ce_workspace(N, V, D, dt, 1), dev, stream)
+    dX = _out(dX, "dX", here, X.dtype, (N, D), dev, stream)
+    dW = _out(dW, "dW", here, X.dtype, (V, D), dev, stream)
+    _check(L.linear_ce_bwd(xp, wp, tp, N, V, D, dt, ep, gp, sp, dX.data_ptr(), dW.data_ptr(), w.data_ptr(), w.numel(),
                            _stream(stream)))
     return dX, dW
 
@@ -627,16 +647,15 @@ def _norm_out(grads, norm, stream):
     dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
     L = load()
     w = _work(L.grad_clip_workspace(len(grads)), dev, stream)
-    norm = _new((1,), torch.float32, dev, stream) if norm is None else norm
-    return L, w, norm, _dev(norm, "norm", torch.float32, (1,))
+    return L, w, _out(norm, "norm", dev.index, torch.float32, (1,), dev, stream)
 
 
 def grad_norm(grads, norm=None, stream=None):
     """The 2-norm of all elements of a list of fp32 and bf16 tensors, as an fp32 tensor [1]."""
     grads = list(grads)
     gp, nn, dt = _host_arrays(_tensor_list(grads, "grads"))
-    L, w, norm, np_ = _norm_out(grads, norm, stream)
-    _check(L.grad_norm(gp, nn, dt, len(grads), np_, c_void_p(w.data_ptr()), w.numel(), _stream(stream)))
+    L, w, norm = _norm_out(grads, norm, stream)
+    _check(L.grad_norm(gp, nn, dt, len(grads), norm.data_ptr(), w.data_ptr(), w.numel(), _stream(stream)))
     return norm
 
 
@@ -647,9 +666,8 @@ def grad_clip(grads, max_norm: float, outs=None, norm=None, stream=None):
     mine = _tensor_list(grads, "grads")
     gp, nn, dt = _host_arrays(mine)
     op = gp if outs is None else _host_arrays(_tensor_list(list(outs), "outs", mine))[0]
-    L, w, norm, np_ = _norm_out(grads, norm, stream)
-    _check(L.grad_clip(gp, op, nn, dt, len(grads), float(max_norm), np_, c_void_p(w.data_ptr()), w.numel(),
-                       _stream(stream)))
+    L, w, norm = _norm_out(grads, norm, stream)
+    _check(L.grad_clip(gp, op, nn, dt, len(grads), float(max_norm), norm.data_ptr(), w.data_ptr(), w.numel(), _stream(stream)))
     return norm
 
 

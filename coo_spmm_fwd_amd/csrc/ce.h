@@ -1,5 +1,5 @@
 // ce.h -- what the two forms of the linear cross entropy share: ce.hip (tiles
-// of many tokens) and ce_few.hip (up to kFewTokens tokens).  Private header.
+// of many tokens) and ce_few.hip (few tokens).  Private header.
 #pragma once
 
 #include "common.h"
@@ -95,7 +95,10 @@ inline unsigned out_blocks(int64_t N, int64_t D)
 }
 }  // namespace
 
-constexpr int64_t kFewTokens = 64;
+// Up to how many tokens: 64 in bf16, 128 in fp32, where the other form copies W.
+constexpr int64_t kFewMost = 128;
+inline bool ce_is_few(int64_t N, int dtype) { return N <= (dtype == CSP_F32 ? 128 : 64); }
+
 size_t ce_few_bytes(int64_t N, int64_t V, int64_t D, int dtype, bool backward);
 csp_status ce_few_fwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D, int dtype,
                       float *loss, float *lse, float *total, char *work, hipStream_t s);

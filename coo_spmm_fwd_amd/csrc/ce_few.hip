@@ -1,4 +1,4 @@
-// ce_few.hip -- linear cross entropy of up to 64 tokens (formulas in ce.hip).
+// ce_few.hip -- linear cross entropy of up to 64 tokens, or 128 in fp32 (formulas in ce.hip).
 //
 // With so few tokens every product is bound by the bytes of W and dW: 2 N
 // operations a byte of bf16 W at N = 64 is 64, where the matrix units and the
@@ -12,6 +12,12 @@
 //             vocabulary rows), k_few_join
 //   backward  k_few_prep, k_few_rows (logits -> P -> dW rows, and P for dX),
 //             k_few_dx, k_ce_out
+//
+// Measured: one token, W 50257 x 768 fp32 (154 MB): rows 34 us, the call 46 of
+// which 12 are the two small kernels and the gaps.  One token, 65536 x 4096 bf16
+// (537 MB): 99 us a call, 5.4 TB/s.  64 tokens on that W: forward 118 us a call;
+// the training step 513 (2.15 GB, 4.2 TB/s; a 4 GiB copy moves 4.8).  32 tokens
+// on the fp32 W: rows 38, backward rows 72 (308 MB), dX 38, the step 175.
 //
 // A wave holds 32 vocabulary rows.  Its logits come out with a vocabulary row
 // a lane (lane % 16) and tokens 4 (lane / 16) + r in the registers, which is
@@ -143,26 +149,32 @@ __global__ __launch_bounds__(kFewThreads) void k_few_prep(const typename E::T *_
                                                           float *__restrict__ loss, float *__restrict__ lse)
 {
     constexpr int P = Form<E>::kPlanes, Q = (NB + 1) / 2;
-    __shared__ int32_t rows[kFewTokens];
+    __shared__ int32_t rows[kFewMost];
     __shared__ int shared_count;
     if (threadIdx.x < 64) {
-        const int n = threadIdx.x;
-        const int64_t t = n < N ? targets[n] : -1;
-        const bool part = t >= 0 && t < V;
-        const uint64_t mask = __ballot(part);
-        const int at = __popcll(mask & lanes_below());
-        if (part) rows[at] = n;
-        if (n == 0) shared_count = __popcll(mask);
-        if (blockIdx.x == 0) {
-            if (part) {
-                list.rows[at] = n;
-                list.tgt[at] = (int32_t)t;
+        int before = 0;
+#pragma unroll
+        for (int n = threadIdx.x; n < (NB > 4 ? 128 : 64); n += 64) {
+            const int64_t t = n < N ? targets[n] : -1;
+            const bool part = t >= 0 && t < V;
+            const uint64_t mask = __ballot(part);
+            const int at = before + __popcll(mask & lanes_below());
+            if (part) rows[at] = n;
+            if (blockIdx.x == 0) {
+                if (part) {
+                    list.rows[at] = n;
+                    list.tgt[at] = (int32_t)t;
+                }
+                if (n < N) {
+                    list.slot[n] = part ? at : -1;
+                    if (!part && loss) loss[n] = lse[n] = 0.0f;
+                }
             }
-            if (n < N) {
-                list.slot[n] = part ? at : -1;
-                if (!part && loss) loss[n] = lse[n] = 0.0f;
-            }
-            if (n == 0) list.count[0] = __popcll(mask);
+            before += __popcll(mask);
+        }
+        if (threadIdx.x == 0) {
+            shared_count = before;
+            if (blockIdx.x == 0) list.count[0] = before;
         }
     }
     __syncthreads();
@@ -219,7 +231,7 @@ struct FewArgs {
 };
 
 template <typename E, int NB, bool kBackward, bool kStream>
-__global__ __launch_bounds__(kFewThreads, 2) void k_few_rows(FewArgs a, const typename E::T *__restrict__ W,
+__global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArgs a, const typename E::T *__restrict__ W,
                                                              typename E::T *__restrict__ dW)
 {
     using T = typename E::T;
@@ -504,12 +516,12 @@ __global__ __launch_bounds__(1024) void k_few_join(const float2 *__restrict__ pa
     __syncthreads();
     if (threadIdx.x >= 64) return;
     double l = 0.0;
-    if (threadIdx.x < kTokens && n < cnt) {
-        const float r = join[0][n].x + logf(join[0][n].y);
-        const float one = r - zt[n];
-        lse[rows[n]] = r;
-        loss[rows[n]] = one;
-        l = one;
+    for (int m = threadIdx.x; m < kTokens && m < cnt; m += 64) {
+        const float r = join[0][m].x + logf(join[0][m].y);
+        const float one = r - zt[m];
+        lse[rows[m]] = r;
+        loss[rows[m]] = one;
+        l += one;
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
@@ -538,7 +550,7 @@ struct FewDx {
 };
 
 template <typename E, int NB>
-__global__ __launch_bounds__(kFewThreads, NB == 4 ? 1 : 2) void k_few_dx(FewDx a, const typename E::T *__restrict__ W)
+__global__ __launch_bounds__(kFewThreads, NB >= 4 ? 1 : 2) void k_few_dx(FewDx a, const typename E::T *__restrict__ W)
 {
     using T = typename E::T;
     constexpr int P = Form<E>::kPlanes, kPer = Form<E>::kPer, C = kDxCols<E>, kStride = C + 4;
@@ -659,17 +671,17 @@ FewPlan few_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward)
         return r;
     };
     const int planes = dtype == CSP_F32 ? 3 : 1;
-    p.nb = N <= 16 ? 1 : N <= 32 ? 2 : 4;
+    p.nb = N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8;
     p.steps = round_up(D, dtype == CSP_F32 ? kChunk<F32> : kChunk<BF16>) / 32;
     p.tiles = ceil_div(V, kFewRows);
-    p.rows = take(4 * kFewTokens);
-    p.tgt = take(4 * kFewTokens);
-    p.slot = take(4 * kFewTokens);
+    p.rows = take(4 * kFewMost);
+    p.tgt = take(4 * kFewMost);
+    p.slot = take(4 * kFewMost);
     p.count = take(4);
     p.Xf = take(p.steps * p.nb * planes * 1024);
     if (!backward) {
         p.part = take(p.tiles * 16 * p.nb * 8);
-        p.zt = take(4 * kFewTokens);
+        p.zt = take(4 * kFewMost);
     } else {
         const int64_t cols = dtype == CSP_F32 ? kDxCols<F32> : kDxCols<BF16>, groups = ceil_div(D, cols);
         p.frags = round_up(D, kFewCols) / 16;
@@ -773,7 +785,8 @@ csp_status ce_few_fwd(const void *X, const void *W, const int64_t *targets, int6
                       float *loss, float *lse, float *total, char *work, hipStream_t s)
 {
     auto run = dtype == CSP_BF16 ? (N <= 16 ? fwd_few<BF16, 1> : N <= 32 ? fwd_few<BF16, 2> : fwd_few<BF16, 4>)
-                                 : (N <= 16 ? fwd_few<F32, 1> : N <= 32 ? fwd_few<F32, 2> : fwd_few<F32, 4>);
+                                 : (N <= 16 ? fwd_few<F32, 1> : N <= 32 ? fwd_few<F32, 2> : N <= 64 ? fwd_few<F32, 4>
+                                                                                                  : fwd_few<F32, 8>);
     return run(X, W, targets, N, V, D, loss, lse, total, work, s);
 }
 
@@ -782,7 +795,8 @@ csp_status ce_few_bwd(const void *X, const void *W, const int64_t *targets, int6
                       hipStream_t s)
 {
     auto run = dtype == CSP_BF16 ? (N <= 16 ? bwd_few<BF16, 1> : N <= 32 ? bwd_few<BF16, 2> : bwd_few<BF16, 4>)
-                                 : (N <= 16 ? bwd_few<F32, 1> : N <= 32 ? bwd_few<F32, 2> : bwd_few<F32, 4>);
+                                 : (N <= 16 ? bwd_few<F32, 1> : N <= 32 ? bwd_few<F32, 2> : N <= 64 ? bwd_few<F32, 4>
+                                                                                                  : bwd_few<F32, 8>);
     return run(X, W, targets, N, V, D, lse, dmean, total, dX, dW, work, s);
 }
 

@@ -372,11 +372,15 @@ __global__ __launch_bounds__(kEmbedThreads) void k_embed_join(EmbedGrad a, int64
     if (p.live) put_row<E, false>(dE + id * a.D + p.col, a.D, s, a.scale);
 }
 
-// k_embed_sort costs ceil(V / kSortIds) * N id reads, the radix sort a dozen launches.  The whole gradient
-// at V 65536, d 64 bf16, range / radix: 8192 tokens 21.7 / 90 us, 65536 64 / 113, 131072 110 / 130, 262144
-// 199 / 158.
-constexpr int64_t kSortReads = (int64_t)1 << 25;
-bool sort_by_range(int64_t N, int64_t V) { return V <= (int64_t)1 << 24 && ceil_div(V, kSortIds) * N <= kSortReads; }
+// k_embed_sort costs N id reads to each of ceil(V / kSortIds) workgroups, more where few ids share the tokens;
+// the radix sort a dozen launches.  The whole gradient at d 64 bf16, range / radix, us: V 65536: 8192 tokens 22 /
+// 90, 65536 64 / 113; V 250000: 8192 37 / 98, 32768 71 / 111, 131072 194 / 133; V 3000: 8192 42 / 86, 32768 80 /
+// 105, 131072 227 / 166; V 200: 8192 73 / 97, 32768 124 / 116.
+constexpr int64_t kSortReads = (int64_t)1 << 25, kSortTokens = (int64_t)1 << 16;
+bool sort_by_range(int64_t N, int64_t V)
+{
+    return V <= (int64_t)1 << 24 && N <= (V < 4096 ? kSortTokens / 2 : kSortTokens) && ceil_div(V, kSortIds) * N <= kSortReads;
+}
 
 struct EmbedPlan {
     size_t key[3], pos[3], ptr, hist, part, total;

@@ -411,7 +411,9 @@ int64_t embed_bwd_workspace(int64_t N, int64_t V, int64_t D, csp_dtype dtype);
  *     total   = {sum of loss, count, sum / max(count, 1)}, over the tokens
  *               that take part
  * loss, lse and total are fp32.  A token that takes no part has loss and lse
- * 0, whatever its row of X holds.
+ * 0, whatever its row of X holds.  fp32 operands enter the products as sums of
+ * three bf16 numbers (24 bits): an infinite element of W, or of a row of X
+ * that takes part, makes the logits it enters NaN.
  */
 csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
                          csp_dtype dtype, float *loss, float *lse, float *total, void *workspace,

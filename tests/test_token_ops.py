@@ -337,9 +337,11 @@ def test_linear_ce(N, V, D, mask, dtype):
 @pytest.mark.parametrize("N,V,D,mask", [(1, 127, 65, "none"), (3, 128, 2100, "some"), (15, 129, 127, "none"),
                                         (16, 31, 1001, "some"), (17, 4097, 768, "some"), (32, 33, 513, "last"),
                                         (40, 700, 2100, "some"), (48, 2049, 36, "all"), (64, 12800, 1024, "some"),
-                                        (64, 5, 4100, "none"), (64, 40, 7, "some"), (61, 9001, 129, "some")])
+                                        (64, 5, 4100, "none"), (64, 40, 7, "some"), (61, 9001, 129, "some"),
+                                        (65, 129, 127, "some"), (100, 700, 2100, "some"), (128, 12800, 512, "none"),
+                                        (128, 5, 4100, "some"), (97, 260, 65, "last"), (111, 4097, 48, "all")])
 def test_linear_ce_few_tokens(N, V, D, mask, dtype):
-    """Up to 64 tokens: parts of a wave's 32 and a workgroup's 128 vocabulary rows, chunks and groups of columns
+    """Up to 64 tokens (128 in fp32): parts of a wave's 32 and a workgroup's 128 vocabulary rows, chunks and groups of columns
     that end inside or at a 16-byte load."""
     got = ce_check(*ce_inputs(N, V, D, dtype, N + 3 * V + D, mask))
     if mask == "all":

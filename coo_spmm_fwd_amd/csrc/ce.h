@@ -46,7 +46,7 @@ __device__ __forceinline__ float grad_scale(const float *dmean, const float *tot
 
 namespace {
 // dX[n] = the sum of the splits' rows of its place in the list (acc[split][place][lda], lda a multiple of
-// 4), scaled and rounded; zeros if it has none.  One thread for 4 columns.
+// 4), scaled and rounded; zeros if it has none.  Without a list (slot), place n.  One thread for 4 columns.
 template <typename E>
 __global__ __launch_bounds__(256) void k_ce_out(const float *__restrict__ acc, int64_t lda, int64_t plane, int splits,
                                                 const int32_t *__restrict__ slot, int64_t N, int64_t D,
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void k_ce_out(const float *__restrict__ acc, i
     const float scale = grad_scale(dmean, total);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
         const int64_t n = i / groups, c = (i - n * groups) * 4;
-        const int m = slot[n];
+        const int64_t m = slot ? slot[n] : n;
         f32x4 s{0.0f, 0.0f, 0.0f, 0.0f};
         if (m >= 0) {
             const float *p = acc + m * lda + c;

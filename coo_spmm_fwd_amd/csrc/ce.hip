@@ -433,8 +433,11 @@ struct WeightGrad {
     const int32_t *count;
     int64_t nv, D;
     const float *dmean, *total;
+    int64_t splits, per;  // per: tokens of a split, a multiple of 64
+    float *acc;           // several splits: their sums, [split][vocabulary][lda]
+    int64_t lda, plane;
 };
-template <typename E>
+template <typename E, bool kSplit>
 __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typename E::T *__restrict__ dW)
 {
     using T = Tile<true, true, kBM, 256, kWavesM<256>, kWavesN<256>>;
@@ -442,13 +445,29 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typenam
     using S = Stage<16 * T::FM, 16 * T::FN / kPass, typename E::T>;
     constexpr int kLds = T::kLds > kTileWaves * S::kBytes ? T::kLds : kTileWaves * S::kBytes;
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
-    const TilePlace at = tile_place(ceil_div(a.D, kBM), ceil_div(a.nv, 256), 1);
+    const TilePlace at = tile_place(ceil_div(a.D, kBM), ceil_div(a.nv, 256), kSplit ? a.splits : 1);
     if (!at.ok) return;
-    const int64_t m0 = at.m * kBM, n0 = at.n * 256, cnt = a.count[0];
-    const TileOperand A{a.X + m0, a.ldx, a.planex, (int32_t)(a.ldx - m0 < kBM ? a.ldx - m0 : kBM)};
-    const TileOperand B{a.P + n0, a.ldp, a.planep, 256};
+    const int64_t m0 = at.m * kBM, n0 = at.n * 256, k0 = kSplit ? at.split * a.per : 0;
+    int64_t depth = round_up(a.count[0], kDepth) - k0;
+    if (kSplit) depth = depth < 0 ? 0 : depth < a.per ? depth : a.per;
+    const TileOperand A{a.X + k0 * a.ldx + m0, a.ldx, a.planex, (int32_t)(a.ldx - m0 < kBM ? a.ldx - m0 : kBM)};
+    const TileOperand B{a.P + k0 * a.ldp + n0, a.ldp, a.planep, 256};
     T tile;
-    tile.run(A, B, round_up(cnt, kDepth), Split<E>::kMany, smem);
+    tile.run(A, B, depth, Split<E>::kMany, smem);
+    if constexpr (kSplit) {
+        const int l = threadIdx.x & 63, g = l >> 4;
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) {
+            const int64_t n = n0 + (T::wave_n() * T::FN + j) * 16 + (l & 15);
+            if (n >= a.nv) continue;
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                const int64_t c = m0 + (T::wave_m() * T::FM + i) * 16 + 4 * g;
+                if (c < a.lda) *(f32x4 *)(a.acc + at.split * a.plane + n * a.lda + c) = tile.acc[i][j];
+            }
+        }
+        return;
+    }
     const float s = grad_scale(a.dmean, a.total);
     const int l = threadIdx.x & 63, g = l >> 4;
     const int64_t mw = m0 + T::wave_m() * (16 * T::FM), nw = n0 + T::wave_n() * (16 * T::FN);
@@ -482,11 +501,31 @@ constexpr int64_t kPieceBytes = (int64_t)512 << 20;
 constexpr int64_t kCopyBytesF32 = (int64_t)1 << 30, kCopyBytesBF16 = (int64_t)256 << 20;
 
 struct CePlan {
-    int64_t npad, ldx, piece, tiles, splits;
+    int64_t npad, ldx, piece, tiles, splits, dw_splits;
     int bn;
     bool copy;  // W is copied, a piece at a time: planes, or rows that are no multiple of 128 bytes
-    size_t rows, tgt, slot, count, X, W, part, zt, P, acc, total;
+    size_t rows, tgt, slot, count, X, W, part, zt, P, acc, dw_acc, total;
 };
+
+// Into how many parts the depth of a product of `tiles` tiles is cut, so that its rounds of 256 (one tile a CU)
+// are full: the number with the least time, counting 1% for each part's sums, up to `most` parts and 512 MiB of
+// sums (bytes each).
+int64_t cuts(int64_t tiles, int64_t most, int64_t bytes)
+{
+    const int64_t room = ((int64_t)512 << 20) / bytes;
+    if (most > room) most = room;
+    if (most > 64) most = 64;
+    int64_t r = 1;
+    double best = 1e30;
+    for (int64_t k = 1; k <= most; ++k) {
+        const double t = (double)ceil_div(tiles * k, 256) / (double)k * (1.0 + 0.01 * (double)k);
+        if (t < best) {
+            best = t;
+            r = k;
+        }
+    }
+    return r;
+}
 
 CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w_aligned)
 {
@@ -500,7 +539,10 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
     const int64_t planes = dtype == CSP_F32 ? kPlanes : 1;
     p.npad = round_up(N > 0 ? N : 1, kPad);
     p.ldx = round_up(D, kDepth);
-    p.bn = N <= 128 ? 128 : 256;
+    // Tiles of 128 tokens for few of them, or where tiles of 256 would leave half of the CUs without work (step, tiles
+    // of 256 / 128: 256 tokens, 30000 x 1024, fp32 617 / 523 us, bf16 153 / 125; 384 tokens 735 / 791 and 174 / 172;
+    // 256 tokens, 65536 x 2048, 1942 / 2124 and 408 / 437).
+    p.bn = N <= 128 || ceil_div(V, kBM) * ceil_div(N, 256) <= 128 ? 128 : 256;
     p.copy = dtype == CSP_F32 || D % kDepth != 0 || !w_aligned;
     p.tiles = ceil_div(V, kBM);
     p.piece = round_up(V, kPad);
@@ -522,21 +564,11 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         p.zt = take(4 * p.npad);
     } else {
         p.P = take(planes * 2 * p.npad * p.piece);
-        // The depth of dX is cut so that the rounds of 256 tiles (one a CU) are full: the number of cuts with
-        // the least time, counting 1% for each cut's sums, within 8 steps of depth a cut and 512 MiB of sums.
-        const int64_t tiles = ceil_div(D, kBM) * ceil_div(p.npad, p.bn);
-        int64_t most = ceil_div(p.piece, 8 * kDepth), room = ((int64_t)512 << 20) / (4 * p.npad * p.ldx);
-        if (most > room) most = room;
-        if (most > 64) most = 64;
-        p.splits = 1;
-        double best = 1e30;
-        for (int64_t k = 1; k <= most; ++k) {
-            const double t = (double)ceil_div(tiles * k, 256) / (double)k * (1.0 + 0.01 * (double)k);
-            if (t < best) {
-                best = t;
-                p.splits = k;
-            }
-        }
+        // an fp32 step of depth is six: its parts may be shorter
+        const int64_t least = dtype == CSP_F32 ? 2 * kDepth : 8 * kDepth;
+        p.splits = cuts(ceil_div(D, kBM) * ceil_div(p.npad, p.bn), ceil_div(p.piece, least), 4 * p.npad * p.ldx);
+        p.dw_splits = cuts(ceil_div(D, kBM) * ceil_div(p.piece, 256), ceil_div(N, least), 4 * p.piece * p.ldx);
+        if (p.dw_splits > 1) p.dw_acc = take(4 * p.dw_splits * p.piece * p.ldx);
         p.acc = take(4 * p.splits * p.npad * p.ldx);
     }
     p.total = at;
@@ -654,9 +686,20 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
             else k_ce_dx<256, kMany><<<gx, kTileThreads, 0, s>>>(d);
             CSP_LAUNCHED("k_ce_dx");
         }
-        const WeightGrad g{P, a.X, p.piece, p.ldx, planep, a.planex, count, a.nv, D, dmean, total};
-        k_ce_dw<E><<<(unsigned)(ceil_div(D, kBM) * ceil_div(a.nv, 256)), kTileThreads, 0, s>>>(g, (T *)dW + v0 * D);
-        CSP_LAUNCHED("k_ce_dw");
+        const WeightGrad g{P, a.X, p.piece, p.ldx, planep, a.planex, count, a.nv, D, dmean, total, p.dw_splits,
+                           round_up(ceil_div(p.npad, p.dw_splits), kDepth), (float *)(w + p.dw_acc), p.ldx,
+                           p.piece * p.ldx};
+        const unsigned gw = (unsigned)(ceil_div(D, kBM) * ceil_div(a.nv, 256) * p.dw_splits);
+        if (p.dw_splits == 1) {
+            k_ce_dw<E, false><<<gw, kTileThreads, 0, s>>>(g, (T *)dW + v0 * D);
+            CSP_LAUNCHED("k_ce_dw");
+        } else {
+            k_ce_dw<E, true><<<gw, kTileThreads, 0, s>>>(g, nullptr);
+            CSP_LAUNCHED("k_ce_dw");
+            k_ce_out<E><<<out_blocks(a.nv, D), 256, 0, s>>>(g.acc, p.ldx, g.plane, (int)p.dw_splits, nullptr, a.nv, D,
+                                                            dmean, total, (T *)dW + v0 * D);
+            CSP_LAUNCHED("k_ce_out");
+        }
     }
     if (N > 0) {
         k_ce_out<E><<<out_blocks(N, D), 256, 0, s>>>((const float *)(w + p.acc), p.ldx, p.npad * p.ldx, (int)p.splits,

@@ -11,10 +11,12 @@
 // of dX are 0 and it adds nothing to dW, whatever its row of X holds.  The
 // tokens that take part are listed first (k_ce_rows) and their rows of X
 // gathered (k_ce_gather); every product runs over that list alone, so masked
-// tokens cost nothing.  The logits are never stored: the forward keeps a
+// tokens cost nothing.  The logits are not stored: the forward keeps a
 // maximum and a sum for each (vocabulary tile, token); the backward recomputes
 // the logits, a piece of the vocabulary at a time, from the saved lse, and
-// keeps P = exp(z - lse) - [v = t] of that piece only.
+// keeps P = exp(z - lse) - [v = t] of that piece only.  (A small vocabulary
+// times few tokens makes too few tiles for 256 CUs: there the width is cut,
+// and the parts' logits, a few MiB in the workspace, are read once more.)
 //
 // All three products run on the tile product of mfma_tile.h, each with the
 // dimension that is contiguous in its output as m, so that a lane holds 4
@@ -33,10 +35,10 @@
 // matrix units are busy 65% of the cycles, at 1.9 GHz.  fp32 at 2048 tokens, 30000
 // x 1024: 2.56 ms a step, 197 TFLOP/s of fp32 (1180 of bf16 products).
 //
-// Up to 64 tokens go to ce_few.hip, where the products are bound by the bytes
-// of W: at 64 tokens bf16 this file took 763 us a step for its 513, at 32
-// tokens fp32 573 for 175; at 65 tokens (30000 x 1024) it takes 105 us bf16, 490
-// fp32, most of the latter for the planes of W.
+// Up to 64 tokens (128 in fp32) go to ce_few.hip, where the products are bound by
+// the bytes of W: at 64 tokens bf16 this file took 763 us a step for its 513, at
+// 32 tokens fp32 573 for 175, at 65 fp32 (30000 x 1024) 490 for 274; at 65 bf16 it
+// takes 105.
 #include "ce.h"
 #include "mfma_tile.h"
 
@@ -327,6 +329,127 @@ struct Stage {
     }
 };
 
+// ---------------------------------------------------------------------------
+// Few tiles of logits (a small vocabulary, or not many tokens): their depth is
+// cut and the parts' logits are kept, a few MiB, for one of two passes over
+// them: loss, or P.
+// ---------------------------------------------------------------------------
+struct Parts {
+    float *z;            // [split][token][ldz]
+    int64_t ldz, plane, splits, per;  // per: depth of a split, a multiple of 64
+};
+template <int BN, bool kMany>
+__global__ __launch_bounds__(kTileThreads, 2) void k_ce_logits(Logits a, Parts z)
+{
+    using T = Tile<false, false, kBM, BN, kWavesM<BN>, kWavesN<BN>>;
+    __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
+    const int64_t cnt = a.count[0];
+    const TilePlace at = tile_place(ceil_div(a.nv, kBM), ceil_div(cnt, BN), z.splits);
+    if (!at.ok) return;
+    const int64_t m0 = at.m * kBM, n0 = at.n * BN, k0 = at.split * z.per;
+    const int64_t depth = a.depth - k0 < z.per ? (a.depth - k0 > 0 ? a.depth - k0 : 0) : z.per;
+    const TileOperand A{a.W + m0 * a.ldw + k0, a.ldw, a.planew, (int32_t)(a.nv - m0 < kBM ? a.nv - m0 : kBM)};
+    const TileOperand B{a.X + n0 * a.ldx + k0, a.ldx, a.planex, BN};
+    T tile;
+    tile.run(A, B, depth, kMany, smem);
+    const int l = threadIdx.x & 63, g = l >> 4;
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) {
+        const int64_t n = n0 + (T::wave_n() * T::FN + j) * 16 + (l & 15);
+        if (n >= cnt) continue;
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+            *(f32x4 *)(z.z + at.split * z.plane + n * z.ldz + m0 + (T::wave_m() * T::FM + i) * 16 + 4 * g) = tile.acc[i][j];
+    }
+}
+
+// 4 logits of a token from v on (of columns past the vocabulary: whatever the tiles wrote there).
+__device__ __forceinline__ f32x4 logits_at(const Parts &z, int64_t n, int64_t v)
+{
+    const float *p = z.z + n * z.ldz + v;
+    f32x4 s = *(const f32x4 *)p;
+    for (int64_t k = 1; k < z.splits; ++k) s += *(const f32x4 *)(p + k * z.plane);
+    return s;
+}
+
+// loss and lse of listed token blockIdx.x.
+__global__ __launch_bounds__(kCeThreads) void k_ce_loss(Parts z, const int32_t *__restrict__ rows,
+                                                        const int32_t *__restrict__ tgt,
+                                                        const int32_t *__restrict__ count, int64_t V,
+                                                        float *__restrict__ loss, float *__restrict__ lse)
+{
+    __shared__ float2 join[kCeThreads / 64];
+    const int64_t n = blockIdx.x;
+    if (n >= count[0]) return;
+    float mx = -INFINITY, s = 0.0f;
+    for (int64_t v = threadIdx.x * 4; v < V; v += kCeThreads * 4) {
+        f32x4 x = logits_at(z, n, v);
+        float up = mx;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (v + r >= V) x[r] = -INFINITY;
+            up = fmaxf(up, x[r]);
+        }
+        const float base = up == -INFINITY ? 0.0f : up;
+        s *= exp_of(mx - base);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s += exp_of(x[r] - base);
+        mx = up;
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const float omx = __shfl_xor(mx, off, 64), os = __shfl_xor(s, off, 64), up = fmaxf(mx, omx);
+        const float base = up == -INFINITY ? 0.0f : up;
+        s = s * exp_of(mx - base) + os * exp_of(omx - base);
+        mx = up;
+    }
+    if ((threadIdx.x & 63) == 0) join[threadIdx.x >> 6] = make_float2(mx, s);
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < kCeThreads / 64; ++w) {
+        const float up = fmaxf(mx, join[w].x), base = up == -INFINITY ? 0.0f : up;
+        s = s * exp_of(mx - base) + join[w].y * exp_of(join[w].x - base);
+        mx = up;
+    }
+    const float r = mx + logf(s);
+    const int64_t t = tgt[n];
+    lse[rows[n]] = r;
+    loss[rows[n]] = r - logits_at(z, n, t & ~(int64_t)3)[t & 3];
+}
+
+// P of row blockIdx.x (planes), zeros for columns past the vocabulary and for tokens past the list, up to the
+// next multiple of 64 (the depth of dW).
+template <bool kMany>
+__global__ __launch_bounds__(kCeThreads) void k_ce_p(Parts z, const int32_t *__restrict__ rows,
+                                                     const int32_t *__restrict__ tgt, const int32_t *__restrict__ count,
+                                                     int64_t V, const float *__restrict__ lse,
+                                                     uint16_t *__restrict__ P, int64_t ldp, int64_t planep)
+{
+    const int64_t n = blockIdx.x, cnt = count[0];
+    if (n >= round_up(cnt, kDepth)) return;
+    const bool on = n < cnt;
+    const float ls = on ? lse[rows[n]] * kLog2e : 0.0f;
+    const int64_t t = on ? tgt[n] : -1;
+    for (int64_t v = threadIdx.x * 4; v < ldp; v += kCeThreads * 4) {
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (on && v < V) {
+            const f32x4 y = logits_at(z, n, v);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (v + r < V) x[r] = exp_less(y[r], ls) - (v + r == t ? 1.0f : 0.0f);
+        }
+        uint32_t b[2][kPlanes];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (kMany) split_pair(x[2 * h], x[2 * h + 1], b[h]);
+            else b[h][0] = pack_bf16(x[2 * h], x[2 * h + 1]);
+        }
+#pragma unroll
+        for (int pl = 0; pl < (kMany ? kPlanes : 1); ++pl)
+            *(uint2 *)(P + pl * planep + n * ldp + v) = make_uint2(b[0][pl], b[1][pl]);
+    }
+}
+
 // P of the piece (planes): P[n][v], zeros for tokens past the list and columns past the piece, so
 // that it can serve as depth up to the next multiple of 64.
 template <int BN, bool kMany>
@@ -500,11 +623,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typenam
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;
 constexpr int64_t kCopyBytesF32 = (int64_t)1 << 30, kCopyBytesBF16 = (int64_t)256 << 20;
 
+// Tiles of logits up to which their depth is cut (step, whole / cut: 51 tiles, 2056 tokens x 707 x 1472, fp32 363 /
+// 231 us, bf16 124 / 119; 4 tiles, 209 x 501 x 2241, 426 / 134 and 125 / 90; 48 tiles, 500 x 3000 x 300, fp32 147 /
+// 133; but 88, 245 x 11095 x 192, 138 / 147 and 108, 300 x 9000 x 1024, 384 / 418).
+constexpr int64_t kFewTiles = 64;
+
 struct CePlan {
-    int64_t npad, ldx, piece, tiles, splits, dw_splits;
+    int64_t npad, ldx, piece, tiles, splits, dw_splits, z_splits;
     int bn;
     bool copy;  // W is copied, a piece at a time: planes, or rows that are no multiple of 128 bytes
-    size_t rows, tgt, slot, count, X, W, part, zt, P, acc, dw_acc, total;
+    size_t rows, tgt, slot, count, X, W, part, zt, P, acc, dw_acc, z, total;
 };
 
 // Into how many parts the depth of a product of `tiles` tiles is cut, so that its rounds of 256 (one tile a CU)
@@ -553,6 +681,11 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
     };
     if (p.copy) limit(dtype == CSP_F32 ? kCopyBytesF32 : kCopyBytesBF16, planes * 2 * p.ldx);
     if (backward) limit(kPieceBytes, planes * 2 * p.npad);
+    // an fp32 step of depth is six: its parts may be shorter
+    const int64_t least = dtype == CSP_F32 ? 2 * kDepth : 8 * kDepth;
+    const int64_t tiles = ceil_div(V, kBM) * ceil_div(N, p.bn), vpad = round_up(V, kPad);
+    p.z_splits = tiles <= kFewTiles && p.piece >= vpad ? cuts(tiles, ceil_div(p.ldx, least), 4 * p.npad * vpad) : 1;
+    if (p.z_splits > 1) p.z = take(4 * p.z_splits * p.npad * vpad);
     p.count = take(4);
     p.rows = take(4 * N);
     p.tgt = take(4 * N);
@@ -564,8 +697,6 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         p.zt = take(4 * p.npad);
     } else {
         p.P = take(planes * 2 * p.npad * p.piece);
-        // an fp32 step of depth is six: its parts may be shorter
-        const int64_t least = dtype == CSP_F32 ? 2 * kDepth : 8 * kDepth;
         p.splits = cuts(ceil_div(D, kBM) * ceil_div(p.npad, p.bn), ceil_div(p.piece, least), 4 * p.npad * p.ldx);
         p.dw_splits = cuts(ceil_div(D, kBM) * ceil_div(p.piece, 256), ceil_div(N, least), 4 * p.piece * p.ldx);
         if (p.dw_splits > 1) p.dw_acc = take(4 * p.dw_splits * p.piece * p.ldx);
@@ -627,6 +758,18 @@ csp_status ce_piece(const CePlan &p, const void *W, int64_t V, int64_t D, int64_
     return CSP_OK;
 }
 
+template <bool kMany>
+csp_status ce_logits(const CePlan &p, const Logits &a, int64_t N, char *w, Parts *z, hipStream_t s)
+{
+    const int64_t ldz = round_up(a.nv, kPad);
+    *z = Parts{(float *)(w + p.z), ldz, p.npad * ldz, p.z_splits, round_up(ceil_div(p.ldx, p.z_splits), kDepth)};
+    const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn) * p.z_splits);
+    if (p.bn == 128) k_ce_logits<128, kMany><<<grid, kTileThreads, 0, s>>>(a, *z);
+    else k_ce_logits<256, kMany><<<grid, kTileThreads, 0, s>>>(a, *z);
+    CSP_LAUNCHED("k_ce_logits");
+    return CSP_OK;
+}
+
 template <typename E>
 csp_status fwd_impl(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D, float *loss,
                     float *lse, float *total, char *w, hipStream_t s)
@@ -642,12 +785,20 @@ csp_status fwd_impl(const void *X, const void *W, const int64_t *targets, int64_
         Logits a;
         st = ce_piece<E>(p, W, V, D, v0, w, &a, s);
         if (st != CSP_OK) return st;
+        if (p.z_splits > 1) {
+            Parts z;
+            st = ce_logits<kMany>(p, a, N, w, &z, s);
+            if (st != CSP_OK) return st;
+            k_ce_loss<<<(unsigned)N, kCeThreads, 0, s>>>(z, rows, a.tgt, count, V, loss, lse);
+            CSP_LAUNCHED("k_ce_loss");
+            break;
+        }
         const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
         if (p.bn == 128) k_ce_stats<128, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
         else k_ce_stats<256, kMany><<<grid, kTileThreads, 0, s>>>(a, part, zt);
         CSP_LAUNCHED("k_ce_stats");
     }
-    if (N > 0) {
+    if (N > 0 && p.z_splits == 1) {
         k_ce_join<<<(unsigned)ceil_div(N, 64), 1024, 0, s>>>(part, zt, rows, count, p.npad, p.tiles, loss, lse);
         CSP_LAUNCHED("k_ce_join");
     }
@@ -676,9 +827,15 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
         if (st != CSP_OK) return st;
         if (N > 0) {
             const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
-            if (p.bn == 128) k_ce_probs<128, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
+            if (p.z_splits > 1) {
+                Parts z;
+                st = ce_logits<kMany>(p, a, N, w, &z, s);
+                if (st != CSP_OK) return st;
+                k_ce_p<kMany><<<(unsigned)round_up(N, kDepth), kCeThreads, 0, s>>>(z, rows, a.tgt, count, V, lse, P,
+                                                                                   p.piece, planep);
+            } else if (p.bn == 128) k_ce_probs<128, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
             else k_ce_probs<256, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
-            CSP_LAUNCHED("k_ce_probs");
+            CSP_LAUNCHED("k_ce_probs or k_ce_p");
             const InputGrad d{P, a.W, p.piece, a.ldw, planep, a.planew, count, a.nv, D, p.splits, per,
                               (float *)(w + p.acc), p.ldx, p.npad * p.ldx, v0 > 0};
             const unsigned gx = (unsigned)(ceil_div(D, kBM) * ceil_div(N, p.bn) * p.splits);

@@ -350,6 +350,19 @@ def test_linear_ce_few_tokens(N, V, D, mask, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V,D,mask", [(129, 500, 2241, "none"), (300, 257, 1100, "some"), (1030, 255, 700, "some"),
+                                        (2056, 707, 1472, "some"), (700, 3, 600, "last"), (4000, 600, 130, "some"),
+                                        (150, 1025, 1030, "all"), (5000, 33, 64, "some"), (260, 1, 1500, "none")])
+def test_linear_ce_cut_along_the_depth(N, V, D, mask, dtype):
+    """Few tiles: the logits' depth (the width), dX's (the vocabulary) and dW's (the tokens) are cut into parts,
+    some of them empty when most targets are masked."""
+    got = ce_check(*ce_inputs(N, V, D, dtype, N + 3 * V + D, mask))
+    if mask == "all":
+        assert not got["dX"].any() and not got["dW"].any() and not got["total"].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_linear_ce_over_several_pieces(dtype):
     """So many logits that the backward goes over the vocabulary in pieces."""
     ce_check(*ce_inputs(3000, 66001, 24, dtype, 9, "some"))

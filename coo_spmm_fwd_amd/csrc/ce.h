@@ -16,6 +16,16 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // exp(x - b) from b log2 e: one operation less, and off by the rounding of b log2 e, which is that of b.
 __device__ __forceinline__ float exp_less(float x, float b2) { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -b2)); }
 
+// {lse, loss} of a token from its target's logit and the maximum and sum of exp(z - maximum) of all others.
+// The target stays out of the sum so that a small loss keeps its digits: with d = the others' log-sum less z,
+// loss = max(d, 0) + log(1 + e^-|d|), off by d's rounding times itself, where lse - z is off by that of lse.
+__device__ __forceinline__ float2 loss_of(float mx, float s, float z)
+{
+    const float rest = mx + logf(s), d = rest - z, l = log1pf(expf(-fabsf(d)));
+    // (nothing besides the target: rest and d are -infinity, and loss is 0)
+    return z == INFINITY ? make_float2(NAN, NAN) : make_float2(fmaxf(rest, z) + l, fmaxf(d, 0.0f) + l);
+}
+
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 

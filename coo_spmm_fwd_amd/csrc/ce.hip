@@ -3,7 +3,7 @@
 //
 //   z[n, v] = sum_c X[n, c] W[v, c]
 //   lse[n]  = log sum_v exp z[n, v] = m + log sum_v exp(z[n, v] - m)
-//   loss[n] = lse[n] - z[n, t_n]
+//   loss[n] = lse[n] - z[n, t_n], from the target's logit and the sum of the others (loss_of in ce.h)
 //   G[n, v] = (exp(z[n, v] - lse[n]) - [v = t_n]) * dmean / count
 //   dX = G W,  dW = G^T X
 //
@@ -185,7 +185,7 @@ __device__ __forceinline__ bool logits_tile(const Logits &a, T &tile, TilePlace 
     return true;
 }
 
-// Per (vocabulary tile, listed token): maximum and sum of exp(z - maximum); the target's logit.
+// Per (vocabulary tile, listed token): maximum and sum of exp(z - maximum) besides the target; its logit.
 template <int BN, bool kMany>
 __global__ __launch_bounds__(kTileThreads, 2) void k_ce_stats(Logits a, float2 *__restrict__ part,
                                                                                 float *__restrict__ zt)
@@ -212,10 +212,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_stats(Logits a, float2 *
                 x[i][r] = tile.acc[i][j][r];
                 if (edge) x[i][r] = 16 * i + r >= valid ? -INFINITY : x[i][r];
             }
-#pragma unroll
-        for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[i][r]);
         // the target's logit: few waves hold one
         const int64_t t64 = n < cnt ? a.tgt[n] - a.v0 - vw - 4 * g : -1;
         const int t = t64 >= 0 && t64 < 16 * T::FM && (t64 & 12) == 0 ? (int)t64 : -1;
@@ -224,9 +220,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_stats(Logits a, float2 *
 #pragma unroll
             for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) z = t == 16 * i + r ? x[i][r] : z;
+                for (int r = 0; r < 4; ++r)
+                    if (t == 16 * i + r) {  // kept apart (loss_of)
+                        z = x[i][r];
+                        x[i][r] = -INFINITY;
+                    }
             if (t >= 0) zt[n] = z;
         }
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[i][r]);
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         const float base = mx == -INFINITY ? 0.0f : mx;  // nothing of the vocabulary in this wave
@@ -281,9 +285,9 @@ __global__ __launch_bounds__(1024) void k_ce_join(const float2 *__restrict__ par
     const float base = mx == -INFINITY ? 0.0f : mx;
     s = 0.0f;
     for (int i = 0; i < 16; ++i) s += join[i][l].y * exp_of(join[i][l].x - base);
-    const float r = mx + logf(s);
-    lse[rows[m]] = r;
-    loss[rows[m]] = r - zt[m];
+    const float2 r = loss_of(mx, s, zt[m]);
+    lse[rows[m]] = r.x;
+    loss[rows[m]] = r.y;
 }
 
 __global__ __launch_bounds__(1024) void k_ce_total(const float *__restrict__ loss, const int32_t *__restrict__ count,
@@ -381,13 +385,14 @@ __global__ __launch_bounds__(kCeThreads) void k_ce_loss(Parts z, const int32_t *
     __shared__ float2 join[kCeThreads / 64];
     const int64_t n = blockIdx.x;
     if (n >= count[0]) return;
+    const int64_t t = tgt[n];
     float mx = -INFINITY, s = 0.0f;
     for (int64_t v = threadIdx.x * 4; v < V; v += kCeThreads * 4) {
         f32x4 x = logits_at(z, n, v);
         float up = mx;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (v + r >= V) x[r] = -INFINITY;
+            if (v + r >= V || v + r == t) x[r] = -INFINITY;  // the target is kept apart (loss_of)
             up = fmaxf(up, x[r]);
         }
         const float base = up == -INFINITY ? 0.0f : up;
@@ -411,10 +416,9 @@ __global__ __launch_bounds__(kCeThreads) void k_ce_loss(Parts z, const int32_t *
         s = s * exp_of(mx - base) + join[w].y * exp_of(join[w].x - base);
         mx = up;
     }
-    const float r = mx + logf(s);
-    const int64_t t = tgt[n];
-    lse[rows[n]] = r;
-    loss[rows[n]] = r - logits_at(z, n, t & ~(int64_t)3)[t & 3];
+    const float2 r = loss_of(mx, s, logits_at(z, n, t & ~(int64_t)3)[t & 3]);
+    lse[rows[n]] = r.x;
+    loss[rows[n]] = r.y;
 }
 
 // P of row blockIdx.x (planes), zeros for columns past the vocabulary and for tokens past the list, up to the

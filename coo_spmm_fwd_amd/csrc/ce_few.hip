@@ -43,10 +43,11 @@ constexpr int kFewCols = 64;                       // columns of dW a step
 
 template <typename E> struct Form;
 template <> struct Form<BF16> {
-    static constexpr int kPlanes = 1, kSteps = 4, kPer = 8;  // depth steps of 32 a chunk; elements of 16 bytes
+    // planes of X and W, and of P; depth steps of 32 a chunk; elements of 16 bytes
+    static constexpr int kPlanes = 1, kPPlanes = 2, kSteps = 4, kPer = 8;
 };
 template <> struct Form<F32> {
-    static constexpr int kPlanes = 3, kSteps = 2, kPer = 4;
+    static constexpr int kPlanes = 3, kPPlanes = 3, kSteps = 2, kPer = 4;
 };
 template <typename E> constexpr int kChunk = 32 * Form<E>::kSteps;  // depth of a chunk: 4 16-byte loads a row and lane
 
@@ -62,28 +63,31 @@ template <typename E> __host__ __device__ constexpr int column_of(int f, int m)
     return Form<E>::kPlanes == 1 ? 32 * (f >> 1) + 8 * (m >> 2) + 4 * (f & 1) + (m & 3) : 16 * f + m;
 }
 
-template <typename E> struct Frag {
-    bf16x8 p[Form<E>::kPlanes];
+template <int kPlanes> struct Planes {
+    bf16x8 p[kPlanes];
 };
+template <typename E> using Frag = Planes<Form<E>::kPlanes>;    // of X or W
+template <typename E> using PFrag = Planes<Form<E>::kPPlanes>;  // of P
 // The 8 elements of a lane from floats.
-template <typename E>
-__device__ __forceinline__ Frag<E> frag_of(const float (&x)[8])
+template <int kPlanes>
+__device__ __forceinline__ Planes<kPlanes> planes_of(const float (&x)[8])
 {
-    Frag<E> f;
-    uint32_t w[Form<E>::kPlanes][4];
+    Planes<kPlanes> f;
+    uint32_t w[kPlanes][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (Form<E>::kPlanes == 1) {
-            w[0][i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-        } else {
+        if constexpr (kPlanes == 3) {
             uint32_t p[3];
             split_pair(x[2 * i], x[2 * i + 1], p);
 #pragma unroll
             for (int k = 0; k < 3; ++k) w[k][i] = p[k];
+        } else {
+            w[0][i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            if constexpr (kPlanes == 2) w[1][i] = pack_bf16(x[2 * i] - low_of(w[0][i]), x[2 * i + 1] - high_of(w[0][i]));
         }
     }
 #pragma unroll
-    for (int k = 0; k < Form<E>::kPlanes; ++k)
+    for (int k = 0; k < kPlanes; ++k)
         f.p[k] = __builtin_bit_cast(bf16x8, u32x4{w[k][0], w[k][1], w[k][2], w[k][3]});
     return f;
 }
@@ -92,10 +96,16 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-// c += A B; of fp32 operands the six plane products above 2^-25 of the whole, small ones first.
+// c += A B; of fp32 operands the six plane products above 2^-25 of the whole, small ones first.  P stands
+// beside bf16 operands in two planes, 16 bits: rounded to 8 it would add to a gradient of few terms, as those
+// of few tokens are, as much error again as the output's own rounding, and the products are not the bound.
 __device__ __forceinline__ f32x4 product(const Frag<BF16> &a, const Frag<BF16> &b, f32x4 c)
 {
     return mma(a.p[0], b.p[0], c);
+}
+__device__ __forceinline__ f32x4 product(const Frag<BF16> &a, const PFrag<BF16> &b, f32x4 c)
+{
+    return mma(a.p[0], b.p[0], mma(a.p[0], b.p[1], c));
 }
 __device__ __forceinline__ f32x4 product(const Frag<F32> &a, const Frag<F32> &b, f32x4 c)
 {
@@ -205,7 +215,7 @@ __global__ __launch_bounds__(kFewThreads) void k_few_prep(const typename E::T *_
     } else {
         return;
     }
-    const Frag<E> f = frag_of<E>(x);
+    const Frag<E> f = planes_of<P>(x);
 #pragma unroll
     for (int p = 0; p < P; ++p) dst[p * 64] = __builtin_bit_cast(u32x4, f.p[p]);
 }
@@ -240,7 +250,7 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
     constexpr int kXLoads = (kXChunk + kFewThreads - 1) / kFewThreads;
     constexpr int kFrags = kFewCols / 16;
     constexpr int kTChunk = kFrags * Q * P * 64, kTLoads = kTChunk / kFewThreads;
-    constexpr int kPWave = NB * P * 64;                         // vectors of a wave's P
+    constexpr int PP = Form<E>::kPPlanes, kPWave = NB * PP * 64;  // vectors of a wave's P
     constexpr int kLds = 2 * kXChunk > (kBackward ? (2 * kTChunk > 4 * kPWave ? 2 * kTChunk : 4 * kPWave) : 0)
                              ? 2 * kXChunk : (2 * kTChunk > 4 * kPWave ? 2 * kTChunk : 4 * kPWave);
     __shared__ u32x4 lds[kLds];
@@ -300,7 +310,7 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
                     float f[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[b][2 * s + (j >> 2)][j & 3]);
-                    wf[b] = frag_of<E>(f);
+                    wf[b] = planes_of<P>(f);
                 }
             }
 #pragma unroll
@@ -350,7 +360,10 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     x[b] = v[b] < V ? acc[b][t][r] : -INFINITY;
-                    if (v[b] == tgt) a.zt[n] = x[b];
+                    if (v[b] == tgt) {  // kept apart (loss_of)
+                        a.zt[n] = x[b];
+                        x[b] = -INFINITY;
+                    }
                     mx = fmaxf(mx, x[b]);
                 }
 #pragma unroll
@@ -372,7 +385,7 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
         }
     } else {
         // P, and its planes: pf[b][pair] with tokens as depth
-        Frag<E> pf[2][Q];
+        PFrag<E> pf[2][Q];
         uint16_t *mine = (uint16_t *)(lds + w * kPWave);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -386,24 +399,24 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
                     if (t < NB && n < count && v[b] < V)
                         x[j] = exp_of(acc[b][t < NB ? t : 0][j & 3] - a.lse[a.rows[n]]) - (v[b] == a.tgt[n] ? 1.0f : 0.0f);
                 }
-                pf[b][u] = frag_of<E>(x);
+                pf[b][u] = planes_of<PP>(x);
                 // the same with vocabulary rows as depth, for dX
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
+                for (int p = 0; p < PP; ++p) {
                     const u32x4 y = __builtin_bit_cast(u32x4, pf[b][u].p[p]);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int t = 2 * u + (j >> 2);
                         if (t >= NB) continue;
                         const int vl = 16 * b + (l & 15), to = 4 * q + (j & 3) + 16 * (vl >> 3);
-                        mine[((t * P + p) * 64 + to) * 8 + (vl & 7)] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
+                        mine[((t * PP + p) * 64 + to) * 8 + (vl & 7)] = (uint16_t)(y[j >> 1] >> (16 * (j & 1)));
                     }
                 }
             }
         lds_barrier();
         u32x4 *out = a.Pf + ((int64_t)blockIdx.x * kFewWaves + w) * kPWave + l;
 #pragma unroll
-        for (int i = 0; i < NB * P; ++i) out[i * 64] = lds[w * kPWave + i * 64 + l];
+        for (int i = 0; i < NB * PP; ++i) out[i * 64] = lds[w * kPWave + i * 64 + l];
         lds_barrier();
 
         // dW[v][c] = scale * sum over tokens of X[n][c] P[n][v], 64 columns at a time
@@ -517,11 +530,10 @@ __global__ __launch_bounds__(1024) void k_few_join(const float2 *__restrict__ pa
     if (threadIdx.x >= 64) return;
     double l = 0.0;
     for (int m = threadIdx.x; m < kTokens && m < cnt; m += 64) {
-        const float r = join[0][m].x + logf(join[0][m].y);
-        const float one = r - zt[m];
-        lse[rows[m]] = r;
-        loss[rows[m]] = one;
-        l += one;
+        const float2 r = loss_of(join[0][m].x, join[0][m].y, zt[m]);
+        lse[rows[m]] = r.x;
+        loss[rows[m]] = r.y;
+        l += r.y;
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
@@ -553,7 +565,7 @@ template <typename E, int NB>
 __global__ __launch_bounds__(kFewThreads, NB >= 4 ? 1 : 2) void k_few_dx(FewDx a, const typename E::T *__restrict__ W)
 {
     using T = typename E::T;
-    constexpr int P = Form<E>::kPlanes, kPer = Form<E>::kPer, C = kDxCols<E>, kStride = C + 4;
+    constexpr int P = Form<E>::kPlanes, PP = Form<E>::kPPlanes, kPer = Form<E>::kPer, C = kDxCols<E>, kStride = C + 4;
     __shared__ __attribute__((aligned(16))) float sum[kFewWaves][16][kStride];
     const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), q = l >> 4;
     // workgroups go round the 8 XCDs and splits are a multiple of 8: all columns of a split meet its P in one L2
@@ -569,20 +581,20 @@ __global__ __launch_bounds__(kFewThreads, NB >= 4 ? 1 : 2) void k_few_dx(FewDx a
     for (int i = 0; i < kPer; ++i)
 #pragma unroll
         for (int t = 0; t < NB; ++t) acc[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto load_p = [&](int64_t v, u32x4 (&p)[NB * P]) {
-        const char *ps = (const char *)(a.Pf + (v >> 5) * (NB * P * 64));
+    auto load_p = [&](int64_t v, u32x4 (&p)[NB * PP]) {
+        const char *ps = (const char *)(a.Pf + (v >> 5) * (NB * PP * 64));
 #pragma unroll
-        for (int i = 0; i < NB * P; ++i) p[i] = *(const u32x4 *)(ps + (uint32_t)(l * 16) + i * 1024);
+        for (int i = 0; i < NB * PP; ++i) p[i] = *(const u32x4 *)(ps + (uint32_t)(l * 16) + i * 1024);
     };
     // a row's address is a scalar, with one offset a lane for all
-    auto load = [&](int s, u32x4 (&r)[8], u32x4 (&p)[NB * P]) {
+    auto load = [&](int s, u32x4 (&r)[8], u32x4 (&p)[NB * PP]) {
         const int64_t v = first + 32 * (int64_t)s;
         load_p(v, p);
         const char *ws = (const char *)(W + v * D + c0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[j] = load16(ws + j * rowbytes + lane_off);
     };
-    auto load_guarded = [&](int s, u32x4 (&r)[8], u32x4 (&p)[NB * P]) {
+    auto load_guarded = [&](int s, u32x4 (&r)[8], u32x4 (&p)[NB * PP]) {
         const int64_t v = first + 32 * (int64_t)s;
         load_p(v, p);
 #pragma unroll
@@ -591,12 +603,12 @@ __global__ __launch_bounds__(kFewThreads, NB >= 4 ? 1 : 2) void k_few_dx(FewDx a
             r[j] = load_edge<E>(W + (u < V ? u : V - 1) * D, col, D);  // P is 0 past V
         }
     };
-    auto multiply = [&](const u32x4 (&r)[8], const u32x4 (&p)[NB * P]) {
-        Frag<E> pf[NB];
+    auto multiply = [&](const u32x4 (&r)[8], const u32x4 (&p)[NB * PP]) {
+        PFrag<E> pf[NB];
 #pragma unroll
         for (int t = 0; t < NB; ++t)
 #pragma unroll
-            for (int k = 0; k < P; ++k) pf[t].p[k] = __builtin_bit_cast(bf16x8, p[t * P + k]);
+            for (int k = 0; k < PP; ++k) pf[t].p[k] = __builtin_bit_cast(bf16x8, p[t * PP + k]);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             Frag<E> wf;
@@ -610,13 +622,13 @@ __global__ __launch_bounds__(kFewThreads, NB >= 4 ? 1 : 2) void k_few_dx(FewDx a
                 float f[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[j][i]);
-                wf = frag_of<E>(f);
+                wf = planes_of<P>(f);
             }
 #pragma unroll
             for (int t = 0; t < NB; ++t) acc[i][t] = product(wf, pf[t], acc[i][t]);
         }
     };
-    u32x4 r0[8], r1[8], p0[NB * P], p1[NB * P];
+    u32x4 r0[8], r1[8], p0[NB * PP], p1[NB * PP];
     const int whole = edge ? 0 : first + 32 * (int64_t)steps <= V ? steps : steps - 1;  // steps without a guard
     if (whole > 0) {
         load(0, r0, p0);
@@ -686,7 +698,7 @@ FewPlan few_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward)
         const int64_t cols = dtype == CSP_F32 ? kDxCols<F32> : kDxCols<BF16>, groups = ceil_div(D, cols);
         p.frags = round_up(D, kFewCols) / 16;
         p.Xt = take(p.frags * ((p.nb + 1) / 2) * planes * 1024);
-        p.Pf = take(p.tiles * kFewWaves * p.nb * planes * 1024);
+        p.Pf = take(p.tiles * kFewWaves * p.nb * (dtype == CSP_F32 ? 3 : 2) * 1024);
         // about two workgroups a CU; a wave has at least one step of 32 rows
         int64_t s = round_up(ceil_div(512, groups), 8);
         if (s > 128) s = 128;

@@ -429,6 +429,31 @@ def test_large_logits_do_not_overflow(dtype, N):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V,D", [(1, 700, 96), (40, 700, 96), (200, 30000, 96), (300, 300, 96)])
+def test_small_losses_keep_their_digits(N, V, D, dtype):
+    """Losses down to 1e-6 beside logits of 20.  loss = log(1 + e^d) with d the others' log-sum less the target's
+    logit moves by sigmoid(d) = 1 - e^-loss for each unit of d, and d is off by the logits' errors, as lse is."""
+    g = gen(37)
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    W = torch.randn(V, D, generator=g, device="cuda").to(dtype)
+    raise_ = torch.linspace(0.1, 0.35, N, device="cuda")[:, None] if N > 1 else torch.full((1, 1), 0.25, device="cuda")
+    X = (W.float()[t] * raise_).to(dtype)
+    loss, lse, total = csp.linear_ce_fwd(X, W, t)
+    Xd, Wd = X.double(), W.double()
+    z = Xd @ Wd.T
+    zt = z.gather(1, t[:, None])[:, 0]
+    others = z.scatter(1, t[:, None], -math.inf)
+    d = torch.logsumexp(others, 1) - zt
+    want = torch.nn.functional.softplus(d)
+    assert want.min() < 1e-3
+    ez = (D + 8) * U32 * (Xd.abs() @ Wd.abs().T).amax(1)
+    off = 2 * ez + (V + 16) * U32 + 4 * U32 * (z.abs().amax(1) + torch.logsumexp(z, 1).abs())
+    within(loss, want, torch.expm1(off) * (1 - torch.exp(-want)) + 8 * U32 * want, "loss")
+    assert (loss[want > 1e-12] > 0).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N", [3, 100])
 def test_gradient_against_differences(N):
     """(f(x + h d) - f(x - h d)) / 2h along random directions.  With logits moved by at most a = h |d.w|

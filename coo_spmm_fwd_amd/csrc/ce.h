@@ -19,11 +19,12 @@ __device__ __forceinline__ float exp_less(float x, float b2) { return __builtin_
 // {lse, loss} of a token from its target's logit and the maximum and sum of exp(z - maximum) of all others.
 // The target stays out of the sum so that a small loss keeps its digits: with d = the others' log-sum less z,
 // loss = max(d, 0) + log(1 + e^-|d|), off by d's rounding times itself, where lse - z is off by that of lse.
+// In fp64: it is done once a token, and mx + log s alone would cost half a step of a number of ten and more.
 __device__ __forceinline__ float2 loss_of(float mx, float s, float z)
 {
-    const float rest = mx + logf(s), d = rest - z, l = log1pf(expf(-fabsf(d)));
+    const double rest = (double)mx + log((double)s), d = rest - (double)z, l = log1p(exp(-fabs(d)));
     // (nothing besides the target: rest and d are -infinity, and loss is 0)
-    return z == INFINITY ? make_float2(NAN, NAN) : make_float2(fmaxf(rest, z) + l, fmaxf(d, 0.0f) + l);
+    return z == INFINITY ? make_float2(NAN, NAN) : make_float2((float)(fmax(rest, (double)z) + l), (float)(fmax(d, 0.0) + l));
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

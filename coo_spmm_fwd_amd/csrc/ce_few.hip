@@ -267,6 +267,14 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
     for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int t = 0; t < NB; ++t) acc[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // Up to 32 tokens: a chunk's products start from zero and are added with the lost digits carried along.  The
+    // loss of a token or two shows each rounding of its logit; over more of them they average out.
+    constexpr bool kExact = NB <= 2;
+    f32x4 sum[2][NB], lost[2][NB];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int t = 0; t < NB; ++t) sum[b][t] = lost[b][t] = acc[b][t];
     const int chunks = (int)((D + kChunk<E> - 1) / kChunk<E>);
     const int turn = (int)((blockIdx.x >> 3) % (unsigned)chunks);
     auto chunk_of = [&](int c) { return c + turn < chunks ? c + turn : c + turn - chunks; };
@@ -299,6 +307,12 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
     };
     auto multiply = [&](int c, const u32x4 (&r)[2][4]) {
         const u32x4 *x = lds + (c & 1) * kXChunk + l;
+        if constexpr (kExact) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int t = 0; t < NB; ++t) acc[b][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             Frag<E> wf[2];
@@ -321,6 +335,16 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
 #pragma unroll
                 for (int b = 0; b < 2; ++b) acc[b][t] = product(xf, wf[b], acc[b][t]);
             }
+        }
+        if constexpr (kExact) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int t = 0; t < NB; ++t) {
+                    const f32x4 y = acc[b][t] - lost[b][t], n = sum[b][t] + y;
+                    lost[b][t] = (n - sum[b][t]) - y;
+                    sum[b][t] = n;
+                }
         }
     };
     {
@@ -346,6 +370,12 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
             lds_barrier();
         }
         lds_barrier();  // LDS is free
+        if constexpr (kExact) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int t = 0; t < NB; ++t) acc[b][t] = sum[b][t];
+        }
     }
 
     const int count = a.count[0];

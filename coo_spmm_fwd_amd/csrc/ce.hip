@@ -30,8 +30,8 @@
 // into three bf16 planes (mfma_tile.h).
 //
 // Measured, 8192 tokens, 65536 x 4096 bf16 (4.4 TFLOP a product): forward
-// logits 3.42 ms (1290 TFLOP/s), backward logits 3.61 (1220), dX 3.45 (1275), dW
-// 3.77 (1165); the library's plain product of that shape reaches 1485.  The
+// logits 3.43 ms (1280 TFLOP/s), backward logits 3.60 (1220), dX 3.43 (1280), dW
+// 3.48 (1265); the library's plain product of that shape reaches 1485.  The
 // matrix units are busy 65% of the cycles, at 1.9 GHz.  fp32 at 2048 tokens, 30000
 // x 1024: 2.56 ms a step, 197 TFLOP/s of fp32 (1180 of bf16 products).
 //

@@ -13,11 +13,11 @@
 //   backward  k_few_prep, k_few_rows (logits -> P -> dW rows, and P for dX),
 //             k_few_dx, k_ce_out
 //
-// Measured: one token, W 50257 x 768 fp32 (154 MB): rows 34 us, the call 46 of
-// which 12 are the two small kernels and the gaps.  One token, 65536 x 4096 bf16
+// Measured: one token, W 50257 x 768 fp32 (154 MB): rows 34 us, the call 48 of
+// which 14 are the two small kernels and the gaps.  One token, 65536 x 4096 bf16
 // (537 MB): 99 us a call, 5.4 TB/s.  64 tokens on that W: forward 118 us a call;
-// the training step 513 (2.15 GB, 4.2 TB/s; a 4 GiB copy moves 4.8).  32 tokens
-// on the fp32 W: rows 38, backward rows 72 (308 MB), dX 38, the step 175.
+// the training step 530 (2.15 GB, 4.1 TB/s; a 4 GiB copy moves 4.8).  32 tokens
+// on the fp32 W: rows 38, backward rows 73 (308 MB), dX 38, the step 178.
 //
 // A wave holds 32 vocabulary rows.  Its logits come out with a vocabulary row
 // a lane (lane % 16) and tokens 4 (lane / 16) + r in the registers, which is
@@ -98,7 +98,8 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c)
 }
 // c += A B; of fp32 operands the six plane products above 2^-25 of the whole, small ones first.  P stands
 // beside bf16 operands in two planes, 16 bits: rounded to 8 it would add to a gradient of few terms, as those
-// of few tokens are, as much error again as the output's own rounding, and the products are not the bound.
+// of few tokens are, as much error again as the output's own rounding (one token: 0.0027 of the norm for 0.0016;
+// 64: 0.0019 for 0.0017), and it costs 7 us of 523 at 64 tokens.
 __device__ __forceinline__ f32x4 product(const Frag<BF16> &a, const Frag<BF16> &b, f32x4 c)
 {
     return mma(a.p[0], b.p[0], c);
@@ -800,7 +801,7 @@ csp_status bwd_few(const void *X, const void *W, const int64_t *targets, int64_t
     a.total = total;
     a.Pf = (u32x4 *)(w + p.Pf);
     // A W past the memory-side cache (256 MB) is not there for k_few_dx anyway, and streaming it leaves the
-    // cache to dW (64 tokens, 537 MB: 546 / 513 us a step plain / streamed; 154 MB: 177 / 190).
+    // cache to dW (64 tokens, 537 MB: 546 / 513 us a step plain / streamed, with P in one plane; 154 MB: 177 / 190).
     if (V * D * (int64_t)sizeof(T) > (int64_t)256 << 20)
         k_few_rows<E, NB, true, true><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
     else

@@ -407,7 +407,8 @@ int64_t embed_bwd_workspace(int64_t N, int64_t V, int64_t D, csp_dtype dtype);
  * linear_ce_fwd -- softmax cross entropy of the logits z = X W^T, X [N, D],
  * W [V, D], against targets [N], without storing the logits:
  *     lse[n]  = log sum_v exp z[n, v]
- *     loss[n] = lse[n] - z[n, targets[n]]
+ *     loss[n] = lse[n] - z[n, targets[n]]   (without the cancellation: small
+ *               losses keep their digits)
  *     total   = {sum of loss, count, sum / max(count, 1)}, over the tokens
  *               that take part
  * loss, lse and total are fp32.  A token that takes no part has loss and lse

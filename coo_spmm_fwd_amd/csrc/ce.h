@@ -49,6 +49,13 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[3])
     p[2] = pack_bf16(a - low_of(p[1]), b - high_of(p[1]));
 }
 
+// Two floats as two pairs of bf16, 16 bits of each: the rest of the first rounding is rounded again.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[2])
+{
+    p[0] = pack_bf16(a, b);
+    p[1] = pack_bf16(a - low_of(p[0]), b - high_of(p[0]));
+}
+
 // dmean / count, with the count that the forward divided by.
 __device__ __forceinline__ float grad_scale(const float *dmean, const float *total)
 {

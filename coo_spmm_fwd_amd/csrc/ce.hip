@@ -24,16 +24,17 @@
 //   logits  m = vocabulary, n = token,      k = width       (W and X by rows)
 //   dX      m = width,      n = token,      k = vocabulary  (W by depth, P by rows)
 //   dW      m = width,      n = vocabulary, k = token       (X and P by depth)
-// In bf16, P is rounded to bf16 to enter the products: its error, 2^-8 of each
-// term at most, is that of the rounding of the outputs, and the scale dmean /
-// count is applied to the fp32 sums after it.  In fp32, X, W and P are split
+// P enters the gradient products as bf16 planes: beside bf16 operands two, off by
+// 2^-16 of each term at most, 1/256 of the rounding of the outputs.  Rounded to bf16
+// alone it put the gradients off by 0.0019 of their norm where the outputs' rounding
+// is 0.0017, and a step took two thirds of the time (8192 tokens 13.7 for 20.6 ms).
+// The scale dmean / count is applied to the fp32 sums.  In fp32, X, W and P are split
 // into three bf16 planes (mfma_tile.h).
 //
 // Measured, 8192 tokens, 65536 x 4096 bf16 (4.4 TFLOP a product): forward
-// logits 3.43 ms (1280 TFLOP/s), backward logits 3.60 (1220), dX 3.43 (1280), dW
-// 3.48 (1265); the library's plain product of that shape reaches 1485.  The
-// matrix units are busy 65% of the cycles, at 1.9 GHz.  fp32 at 2048 tokens, 30000
-// x 1024: 2.56 ms a step, 197 TFLOP/s of fp32 (1180 of bf16 products).
+// logits 3.43 ms (1280 TFLOP/s), backward logits 3.60 (1220), dX and dW 7 each for
+// two products; the library's plain product of that shape reaches 1485.  fp32 at
+// 2048 tokens, 30000 x 1024: 2.59 ms a step, 197 TFLOP/s of fp32 (1180 of bf16 products).
 //
 // Up to 64 tokens (128 in fp32) go to ce_few.hip, where the products are bound by
 // the bytes of W: at 64 tokens bf16 this file took 763 us a step for its 513, at
@@ -56,6 +57,10 @@ template <> struct Split<BF16> {
 template <> struct Split<F32> {
     static constexpr bool kMany = true;
 };
+// Plane products of the logits, and of the gradients; planes of P.
+template <bool kMany> constexpr int kLogitProducts = kMany ? kPlaneProducts : 1;
+template <bool kMany> constexpr int kGradProducts = kMany ? kPlaneProducts : 2;
+template <bool kMany> constexpr int kPPlanes = kMany ? kPlanes : 2;
 // Tokens that take part, in order: rows[0 .. count) and their targets tgt; slot[n] = place in that
 // list, or -1.  Clears loss and lse (if given) of the others.  One workgroup.
 __global__ __launch_bounds__(1024) void k_ce_rows(const int64_t *__restrict__ targets, int64_t N, int64_t V,
@@ -181,7 +186,7 @@ __device__ __forceinline__ bool logits_tile(const Logits &a, T &tile, TilePlace 
     const int64_t m0 = at.m * kBM, n0 = at.n * BN;
     const TileOperand A{a.W + m0 * a.ldw, a.ldw, a.planew, (int32_t)(a.nv - m0 < kBM ? a.nv - m0 : kBM)};
     const TileOperand B{a.X + n0 * a.ldx, a.ldx, a.planex, BN};
-    tile.run(A, B, a.depth, kMany, smem);
+    tile.run(A, B, a.depth, kLogitProducts<kMany>, smem);
     return true;
 }
 
@@ -355,7 +360,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_logits(Logits a, Parts z
     const TileOperand A{a.W + m0 * a.ldw + k0, a.ldw, a.planew, (int32_t)(a.nv - m0 < kBM ? a.nv - m0 : kBM)};
     const TileOperand B{a.X + n0 * a.ldx + k0, a.ldx, a.planex, BN};
     T tile;
-    tile.run(A, B, depth, kMany, smem);
+    tile.run(A, B, depth, kLogitProducts<kMany>, smem);
     const int l = threadIdx.x & 63, g = l >> 4;
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {
@@ -442,14 +447,11 @@ __global__ __launch_bounds__(kCeThreads) void k_ce_p(Parts z, const int32_t *__r
             for (int r = 0; r < 4; ++r)
                 if (v + r < V) x[r] = exp_less(y[r], ls) - (v + r == t ? 1.0f : 0.0f);
         }
-        uint32_t b[2][kPlanes];
+        uint32_t b[2][kPPlanes<kMany>];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if constexpr (kMany) split_pair(x[2 * h], x[2 * h + 1], b[h]);
-            else b[h][0] = pack_bf16(x[2 * h], x[2 * h + 1]);
-        }
+        for (int h = 0; h < 2; ++h) split_pair(x[2 * h], x[2 * h + 1], b[h]);
 #pragma unroll
-        for (int pl = 0; pl < (kMany ? kPlanes : 1); ++pl)
+        for (int pl = 0; pl < kPPlanes<kMany>; ++pl)
             *(uint2 *)(P + pl * planep + n * ldp + v) = make_uint2(b[0][pl], b[1][pl]);
     }
 }
@@ -474,7 +476,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_probs(Logits a,
     const int64_t cnt = a.count[0], vw = at.m * kBM + wm * (16 * T::FM), nw = at.n * BN + wn * (16 * T::FN);
     const int valid = (int)(a.nv - vw < 16 * T::FM ? a.nv - vw : 16 * T::FM) - 4 * g;  // rows from the lane's first on
     const bool edge = a.nv - vw < 16 * T::FM || nw + 16 * T::FN > cnt;
-    constexpr int kOut = kMany ? kPlanes : 1;
+    constexpr int kOut = kPPlanes<kMany>;
     char *mine = smem + (threadIdx.x >> 6) * (kOut * S::kBytes);
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {  // 16 tokens at a time
@@ -496,12 +498,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_probs(Logits a,
             if (edge)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[r] = 16 * i + r < end ? x[r] : 0.0f;
-            uint32_t b[2][kPlanes];
+            uint32_t b[2][kOut];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (kMany) split_pair(x[2 * h], x[2 * h + 1], b[h]);
-                else b[h][0] = pack_bf16(x[2 * h], x[2 * h + 1]);
-            }
+            for (int h = 0; h < 2; ++h) split_pair(x[2 * h], x[2 * h + 1], b[h]);
 #pragma unroll
             for (int pl = 0; pl < kOut; ++pl)
                 *(uint2 *)(mine + pl * S::kBytes + (l & 15) * S::kStride + (16 * i + 4 * g) * 2) =
@@ -538,7 +537,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dx(InputGrad a)
     const TileOperand A{a.W + k0 * a.ldw + m0, a.ldw, a.planew, (int32_t)(a.ldw - m0 < kBM ? a.ldw - m0 : kBM)};
     const TileOperand B{a.P + n0 * a.ldp + k0, a.ldp, a.planep, BN};
     T tile;
-    tile.run(A, B, depth, kMany, smem);
+    tile.run(A, B, depth, kGradProducts<kMany>, smem);
     const int l = threadIdx.x & 63, g = l >> 4;
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {
@@ -580,7 +579,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typenam
     const TileOperand A{a.X + k0 * a.ldx + m0, a.ldx, a.planex, (int32_t)(a.ldx - m0 < kBM ? a.ldx - m0 : kBM)};
     const TileOperand B{a.P + k0 * a.ldp + n0, a.ldp, a.planep, 256};
     T tile;
-    tile.run(A, B, depth, Split<E>::kMany, smem);
+    tile.run(A, B, depth, kGradProducts<Split<E>::kMany>, smem);
     if constexpr (kSplit) {
         const int l = threadIdx.x & 63, g = l >> 4;
 #pragma unroll
@@ -668,7 +667,7 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         at += (size_t)round_up(bytes, 1024);
         return r;
     };
-    const int64_t planes = dtype == CSP_F32 ? kPlanes : 1;
+    const int64_t planes = dtype == CSP_F32 ? kPlanes : 1, p_planes = dtype == CSP_F32 ? kPPlanes<true> : kPPlanes<false>;
     p.npad = round_up(N > 0 ? N : 1, kPad);
     p.ldx = round_up(D, kDepth);
     // Tiles of 128 tokens for few of them, or where tiles of 256 would leave half of the CUs without work (step, tiles
@@ -684,7 +683,7 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         if (r < p.piece) p.piece = r;
     };
     if (p.copy) limit(dtype == CSP_F32 ? kCopyBytesF32 : kCopyBytesBF16, planes * 2 * p.ldx);
-    if (backward) limit(kPieceBytes, planes * 2 * p.npad);
+    if (backward) limit(kPieceBytes, p_planes * 2 * p.npad);
     // an fp32 step of depth is six: its parts may be shorter
     const int64_t least = dtype == CSP_F32 ? 2 * kDepth : 8 * kDepth;
     const int64_t tiles = ceil_div(V, kBM) * ceil_div(N, p.bn), vpad = round_up(V, kPad);
@@ -700,7 +699,7 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         p.part = take(8 * p.npad * p.tiles);
         p.zt = take(4 * p.npad);
     } else {
-        p.P = take(planes * 2 * p.npad * p.piece);
+        p.P = take(p_planes * 2 * p.npad * p.piece);
         p.splits = cuts(ceil_div(D, kBM) * ceil_div(p.npad, p.bn), ceil_div(p.piece, least), 4 * p.npad * p.ldx);
         p.dw_splits = cuts(ceil_div(D, kBM) * ceil_div(p.piece, 256), ceil_div(N, least), 4 * p.piece * p.ldx);
         if (p.dw_splits > 1) p.dw_acc = take(4 * p.dw_splits * p.piece * p.ldx);

@@ -76,15 +76,11 @@ __device__ __forceinline__ Planes<kPlanes> planes_of(const float (&x)[8])
     uint32_t w[kPlanes][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (kPlanes == 3) {
-            uint32_t p[3];
-            split_pair(x[2 * i], x[2 * i + 1], p);
+        uint32_t p[kPlanes];
+        if constexpr (kPlanes == 1) p[0] = pack_bf16(x[2 * i], x[2 * i + 1]);
+        else split_pair(x[2 * i], x[2 * i + 1], p);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) w[k][i] = p[k];
-        } else {
-            w[0][i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-            if constexpr (kPlanes == 2) w[1][i] = pack_bf16(x[2 * i] - low_of(w[0][i]), x[2 * i + 1] - high_of(w[0][i]));
-        }
+        for (int k = 0; k < kPlanes; ++k) w[k][i] = p[k];
     }
 #pragma unroll
     for (int k = 0; k < kPlanes; ++k)

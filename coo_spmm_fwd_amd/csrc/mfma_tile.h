@@ -29,7 +29,7 @@
 // plane the rest rounded to nearest, 24 bits in all.  Six of the nine plane
 // products are taken; the three left out are below 2^-25 of |x w|, under the
 // rounding of the fp32 sum itself.  They are walked as six pairs of steps in
-// place of one.
+// place of one.  An operand B of two planes beside a single A takes the first two.
 #pragma once
 
 #include <type_traits>
@@ -50,7 +50,7 @@ constexpr int kSlots = 5;
 constexpr int kTileWaves = 8;
 constexpr int kTileThreads = 64 * kTileWaves;
 constexpr int kPlanes = 3;        // planes of an fp32 operand
-constexpr int kPlaneProducts = 6;
+constexpr int kPlaneProducts = 6; // (A, B) planes (0, 0), (0, 1), (1, 0), (1, 1), (0, 2), (2, 0)
 
 // One operand of a tile.  rows: valid rows (r) from the tile's first on;
 // loads past them repeat the last one.  For kDepthMajor, ld - (first r) bounds
@@ -235,8 +235,8 @@ struct Tile {
     }
 
     // depth: valid k (operands with k along their rows are readable, and zero on one side, up to a
-    // multiple of 64); planes: whether the operands are fp32 in planes.
-    __device__ __forceinline__ void run(const TileOperand &A, const TileOperand &B, int64_t depth, bool planes,
+    // multiple of 64); segs: how many of the plane products are taken (1, 2 or all).
+    __device__ __forceinline__ void run(const TileOperand &A, const TileOperand &B, int64_t depth, int segs,
                                         char *smem)
     {
         const uint32_t lds = (uint32_t)(uintptr_t)(lds_char *)smem;
@@ -249,7 +249,6 @@ struct Tile {
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int segs = planes ? kPlaneProducts : 1;
         const int steps = (int)((depth + kDepth - 1) / kDepth) * segs * 2;  // even
         if (steps == 0) return;
         const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
@@ -260,7 +259,7 @@ struct Tile {
         // two.  No branch: the loops below are single blocks, in which the sums keep their registers.
         auto next = [&](auto odd) {
             constexpr int kOdd = decltype(odd)::value;
-            const int qa = planes ? 0x850 >> (2 * seg) & 3 : 0, qb = planes ? 0x244 >> (2 * seg) & 3 : 0;
+            const int qa = segs > 2 ? 0x850 >> (2 * seg) & 3 : 0, qb = segs > 1 ? 0x244 >> (2 * seg) & 3 : 0;
             const int64_t k = k0 + kOdd * kStep, kd = k < depth ? k : depth - 1;
             pa = uniform_ptr(A.base + qa * A.plane + (kADepth ? kd * A.ld : k));
             pb = uniform_ptr(B.base + qb * B.plane + (kBDepth ? kd * B.ld : k));

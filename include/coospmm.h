@@ -379,7 +379,7 @@ csp_status sparse_layer_time_next(sparse_layer_t layer, void *ev_before, void *e
  * steps to the surrounding model).  They need no layer.  Token ids and targets
  * are int64 device arrays; an id or target outside [0, V) takes no part.
  * dtype is the type of the named matrices; sums are fp32, and each output is
- * rounded once.  A call that needs scratch memory takes a device workspace of
+ * rounded once (what else linear_ce rounds stands there).  A call that needs scratch memory takes a device workspace of
  * the caller (16-byte aligned, at least the bytes its _workspace function
  * says, contents undefined before and after).  All are asynchronous on
  * "stream", allocate nothing and may be captured in a HIP graph.  No float
@@ -427,7 +427,9 @@ csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, i
  * with lse and total as linear_ce_fwd left them and dmean one fp32 on the
  * device.  The logits are recomputed a piece of the vocabulary at a time.
  * Rows of dX of tokens that take no part are 0 and such tokens add nothing to
- * dW.  dX and dW have the dtype of X and W.
+ * dW.  dX and dW have the dtype of X and W.  exp(z - lse) - [v = t] enters the
+ * products with bf16 operands as a sum of two bf16 numbers (off by 2^-16 of
+ * itself at most), with fp32 operands as a sum of three.
  */
 csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
                          csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX, void *dW,

@@ -1,0 +1,68 @@
+"""What the linear cross entropy and its gradient hold on to: the digits of P, of small losses and of
+long sums, and infinite logits, against 64-bit forms.
+
+u(t) = finfo(t).eps / 2 is the largest relative error of one rounding to t.
+"""
+import math
+
+import pytest
+import torch
+
+from coo_spmm_fwd_amd import binding as csp
+from coo_spmm_fwd_amd import token_ops as ops
+from tests.test_token_ops import BF16, F32, U32, ce_inputs, gen, u, within
+
+# P stands beside bf16 operands as a sum of two bf16 numbers: the rest of the first rounding, 2^-8 of P
+# at most, is rounded again.  Beside fp32 operands three of them hold all 24 bits.
+P_ERROR = {BF16: u(BF16) ** 2, F32: 0.0}
+
+
+def gradient_reference(X, W, t, target_error=None):
+    """dX and dW of the mean loss in 64 bits, and how far fp32 sums and P_ERROR may put them off.
+    target_error: relative error of the target's element of G, otherwise that of p - 1."""
+    N, V, D = X.shape[0], W.shape[0], X.shape[1]
+    rows = ((t >= 0) & (t < V)).nonzero()[:, 0]
+    at = (torch.arange(rows.numel(), device="cuda"), t[rows])
+    Xd, Wd = X.double()[rows], W.double()
+    z = Xd @ Wd.T
+    lse = torch.logsumexp(z, 1)
+    ez = (D + 8) * U32 * (Xd.abs() @ Wd.abs().T)
+    el = ez.amax(1) + (V + 16) * U32 + 4 * U32 * (z.abs().amax(1) + lse.abs())
+    G = torch.exp(z - lse[:, None])
+    dG = G * (torch.expm1(ez + el[:, None]) + 8 * U32)
+    zt = z[at]
+    G[at] = torch.expm1(-torch.nn.functional.softplus(torch.logsumexp(z.index_put(at, torch.full_like(zt, -math.inf)), 1) - zt))
+    dG = dG + U32 * G.abs()
+    if target_error is not None:
+        dG[at] = (target_error(ez, z, lse) + 8 * U32) * G[at].abs()
+    dG = dG + P_ERROR[X.dtype] * (G.abs() + dG)
+    k = 1.0 / max(1, rows.numel())
+    dX, eX = torch.zeros(2, N, D, dtype=torch.float64, device="cuda")
+    dX[rows] = G @ Wd * k
+    eX[rows] = (dG @ Wd.abs() + (V + 8) * U32 * (G.abs() @ Wd.abs())) * k
+    Gt, dGt = G.T.contiguous(), dG.T.contiguous()
+    dW = Gt @ Xd * k
+    eW = (dGt @ Xd.abs() + (rows.numel() + 8) * U32 * (Gt.abs() @ Xd.abs())) * k
+    uo = u(X.dtype)
+    return dX, eX + uo * (dX.abs() + eX), dW, eW + uo * (dW.abs() + eW)
+
+
+def gradients(X, W, t):
+    X, W = X.clone().requires_grad_(), W.clone().requires_grad_()
+    ops.linear_cross_entropy(X, W, t).backward()
+    return X.grad, W.grad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V,D,mask", [(1, 300, 64, "none"), (16, 129, 40, "some"), (33, 260, 96, "none"),
+                                        (64, 300, 64, "some"), (65, 300, 64, "none"), (128, 257, 100, "some"),
+                                        (129, 300, 64, "none"), (200, 4000, 64, "none"), (600, 40, 32, "some"),
+                                        (300, 9000, 33, "some"), (1500, 20000, 64, "none")])
+def test_gradients_hold_the_digits_of_p(N, V, D, mask, dtype):
+    """Each form (few tokens, logits kept in parts, tiles): one rounding of P to bf16 would show."""
+    X, W, t = ce_inputs(N, V, D, dtype, N + V + D, mask)
+    dX, eX, dW, eW = gradient_reference(X, W, t)
+    gX, gW = gradients(X, W, t)
+    within(gX, dX, eX, "dX")
+    within(gW, dW, eW, "dW")

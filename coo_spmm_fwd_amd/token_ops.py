@@ -6,8 +6,7 @@ entropy and gradient clipping (the library's embed_*, linear_ce_* and grad_* cal
     norm = clip_grad_norm(params, max_norm)   # scales .grad in place, returns the norm before
 
 ids and targets outside [0, V) take no part: padding rows are zero and masked tokens (-100, say)
-cost nothing and get zero gradients.  The gradients have no gradients of their own: to differentiate
-them (a penalty on a gradient, say) raises an error.  Nothing here reads back to the host, so a step made of these
+cost nothing and get zero gradients.  Nothing here reads back to the host, so a step made of these
 can be captured in a HIP graph; as with any autograd capture, drop the losses and gradients of eager
 steps on the same parameters first (their graph holds the parameters' accumulation nodes on the
 eager stream).
@@ -17,7 +16,6 @@ Argument marshalling only: every step runs in the HIP library.
 from __future__ import annotations
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import binding as csp
 
@@ -30,7 +28,6 @@ class _Embedding(torch.autograd.Function):
         return csp.embed_fwd(E, ids, scale)
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dY):
         (ids,) = ctx.saved_tensors
         return csp.embed_bwd(dY.contiguous(), ids, ctx.vocab, ctx.scale), None, None
@@ -44,7 +41,6 @@ class _LinearCrossEntropy(torch.autograd.Function):
         return total[2].clone()  # the backward reads total; the caller may change its loss in place
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dmean):
         X, W, targets, lse, total = ctx.saved_tensors
         dX, dW = csp.linear_ce_bwd(X, W, targets, lse, dmean.reshape(1).contiguous(), total)

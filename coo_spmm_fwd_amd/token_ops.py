@@ -6,7 +6,8 @@ entropy and gradient clipping (the library's embed_*, linear_ce_* and grad_* cal
     norm = clip_grad_norm(params, max_norm)   # scales .grad in place, returns the norm before
 
 ids and targets outside [0, V) take no part: padding rows are zero and masked tokens (-100, say)
-cost nothing and get zero gradients.  Nothing here reads back to the host, so a step made of these
+cost nothing and get zero gradients.  Second derivatives pass through embedding; the gradients of
+linear_cross_entropy have none, and differentiating them raises an error.  Nothing here reads back to the host, so a step made of these
 can be captured in a HIP graph; as with any autograd capture, drop the losses and gradients of eager
 steps on the same parameters first (their graph holds the parameters' accumulation nodes on the
 eager stream).
@@ -30,7 +31,22 @@ class _Embedding(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dY):
         (ids,) = ctx.saved_tensors
-        return csp.embed_bwd(dY.contiguous(), ids, ctx.vocab, ctx.scale), None, None
+        return _EmbeddingGrad.apply(dY.contiguous(), ids, ctx.vocab, ctx.scale), None, None
+
+
+class _EmbeddingGrad(torch.autograd.Function):
+    """dE of dY, which is linear in it: its own gradient is the lookup."""
+
+    @staticmethod
+    def forward(ctx, dY, ids, vocab, scale):
+        ctx.save_for_backward(ids)
+        ctx.scale = scale
+        return csp.embed_bwd(dY, ids, vocab, scale)
+
+    @staticmethod
+    def backward(ctx, ddE):
+        (ids,) = ctx.saved_tensors
+        return _Embedding.apply(ddE.contiguous(), ids, ctx.scale), None, None, None
 
 
 class _LinearCrossEntropy(torch.autograd.Function):
@@ -43,8 +59,21 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dmean):
         X, W, targets, lse, total = ctx.saved_tensors
-        dX, dW = csp.linear_ce_bwd(X, W, targets, lse, dmean.reshape(1).contiguous(), total)
+        dX, dW = _LinearCrossEntropyGrad.apply(X, W, targets, lse, dmean.reshape(1).contiguous(), total)
         return dX, dW, None
+
+
+class _LinearCrossEntropyGrad(torch.autograd.Function):
+    """dX and dW.  Under create_graph=True they hang on X, W and dmean, so that differentiating them (a penalty
+    on a gradient, say) arrives here; otherwise they would pass for constants and their part be dropped."""
+
+    @staticmethod
+    def forward(ctx, X, W, targets, lse, dmean, total):
+        return csp.linear_ce_bwd(X, W, targets, lse, dmean, total)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the gradients of linear_cross_entropy cannot be differentiated")
 
 
 def embedding(ids, E, scale: float = 1.0):

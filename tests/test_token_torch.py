@@ -1,0 +1,81 @@
+"""The torch functions of token_ops.py under autograd's and clipping's own rules, on the CPU: the library's
+calls are replaced by plain torch ones, so what is tested is what the functions make of them."""
+import pytest
+import torch
+
+from coo_spmm_fwd_amd import token_ops as ops
+
+
+@torch.no_grad()  # as the library: torch sees no part of it
+def plain_embed_fwd(E, ids, scale):
+    return E[ids] * scale
+
+
+@torch.no_grad()
+def plain_embed_bwd(dY, ids, V, scale):
+    return torch.zeros(V, dY.shape[1]).index_add_(0, ids, dY * scale)
+
+
+@torch.no_grad()
+def plain_ce_fwd(X, W, t):
+    z = X @ W.T
+    lse = torch.logsumexp(z, 1)
+    loss = lse - z.gather(1, t[:, None])[:, 0]
+    return loss, lse, torch.stack([loss.sum(), torch.tensor(float(t.numel())), loss.mean()])
+
+
+@torch.no_grad()
+def plain_ce_bwd(X, W, t, lse, dmean, total, **more):
+    G = torch.exp(X @ W.T - lse[:, None])
+    G[torch.arange(t.numel()), t] -= 1.0
+    G = G * dmean / total[1]
+    need = more.get("need", (True, True))
+    return G @ W if need[0] else None, G.T @ X if need[1] else None
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    monkeypatch.setattr(ops.csp, "embed_fwd", plain_embed_fwd)
+    monkeypatch.setattr(ops.csp, "embed_bwd", plain_embed_bwd)
+    monkeypatch.setattr(ops.csp, "linear_ce_fwd", plain_ce_fwd)
+    monkeypatch.setattr(ops.csp, "linear_ce_bwd", plain_ce_bwd)
+
+
+def leaves():
+    g = torch.Generator().manual_seed(0)
+    X, W = (torch.randn(n, 5, generator=g).requires_grad_() for n in (4, 7))
+    return X, W, torch.tensor([0, 6, 2, 2])
+
+
+def test_first_gradients_agree_with_torch(plain):
+    X, W, t = leaves()
+    mine = torch.autograd.grad(ops.linear_cross_entropy(X, W, t), (X, W))
+    want = torch.autograd.grad(torch.nn.functional.cross_entropy(X @ W.T, t), (X, W))
+    assert all(torch.allclose(a, b, atol=1e-6) for a, b in zip(mine, want))
+    (mine,) = torch.autograd.grad(ops.embedding(t, W, 2.0).square().sum(), W)
+    (want,) = torch.autograd.grad((W[t] * 2.0).square().sum(), W)
+    assert torch.allclose(mine, want)
+
+
+def test_second_gradients_of_the_loss_raise(plain):
+    """A penalty on a gradient differentiates the backward pass, which has no derivative of its own: an error,
+    never a gradient without the penalty's part."""
+    X, W, t = leaves()
+    loss = ops.linear_cross_entropy(X, W, t)
+    gX, gW = torch.autograd.grad(loss, (X, W), create_graph=True)
+    for g in (gX, gW):
+        with pytest.raises(RuntimeError, match="cannot be differentiated"):
+            torch.autograd.grad(loss + g.square().sum(), (X, W), retain_graph=True)
+    gX, gW = torch.autograd.grad(loss, (X, W))   # and no graph where none was asked for
+    assert not gX.requires_grad and not gW.requires_grad
+
+
+def test_second_gradients_pass_through_the_embedding(plain):
+    for f in (ops.embedding, lambda ids, E, scale: E[ids] * scale):
+        _, E, ids = leaves()
+        y = f(ids, E, 2.0)
+        (g,) = torch.autograd.grad(y.pow(3).sum(), E, create_graph=True)
+        (second,) = torch.autograd.grad(y.sum() + g.square().sum(), E)
+        if f is ops.embedding:
+            mine = second
+    assert torch.allclose(mine, second)

@@ -661,7 +661,8 @@ def grad_norm(grads, norm=None, stream=None):
 
 def grad_clip(grads, max_norm: float, outs=None, norm=None, stream=None):
     """Multiply every tensor by min(1, max_norm / (norm + 1e-6)), in place or into `outs`; returns
-    the norm before clipping, as an fp32 tensor [1] (nothing is read back to the host)."""
+    the norm before clipping, as an fp32 tensor [1] (nothing is read back to the host).  Tensors that
+    overlap, or one listed twice, are an error."""
     grads = list(grads)
     mine = _tensor_list(grads, "grads")
     gp, nn, dt = _host_arrays(mine)

@@ -20,6 +20,10 @@
 // order with 2048 workgroups of 16 KiB chunks); 400 tensors of both types, 500
 // million elements, 822 us (1067).  For 3 tensors of 1.9 MB the call is 19 us
 // of host work, for hundreds 0.45 us a tensor.
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "common.h"
 #include "device_util.h"
 
@@ -259,6 +263,40 @@ ClipPlan clip_plan(int64_t count)
     return p;
 }
 
+// Outputs share no byte with each other, nor with any gradient but their own in place: workgroups read and
+// write in no order.  Sorted by address, each has to end before the next begins (400 tensors: about 10 us of
+// the call's 180 on the host).
+struct Span {
+    uintptr_t first, last;
+    int64_t i;
+};
+csp_status outputs_apart(const void *const *grads, void *const *outs, const int64_t *numel, const int32_t *dtypes,
+                         int64_t count)
+{
+    std::unique_ptr<Span[]> w(new (std::nothrow) Span[(size_t)count]);
+    if (!w) return set_error(CSP_ERR_NO_MEMORY, "no host memory for %lld tensors", (long long)count);
+    auto span = [&](const void *p, int64_t i) {
+        return Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)numel[i] * (dtypes[i] == CSP_BF16 ? 2 : 4), i};
+    };
+    auto overlap = [&](int64_t a, int64_t b) {
+        return set_error(CSP_ERR_INVALID_ARG, "tensors %lld and %lld overlap", (long long)a, (long long)b);
+    };
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i)
+        if (numel[i] > 0) w[n++] = span(outs[i], i);
+    std::sort(w.get(), w.get() + n, [](const Span &a, const Span &b) { return a.first < b.first; });
+    for (int64_t k = 1; k < n; ++k)
+        if (w[k].first < w[k - 1].last) return overlap(w[k - 1].i, w[k].i);
+    for (int64_t i = 0; i < count; ++i) {
+        if (numel[i] == 0 || grads[i] == outs[i]) continue;  // in place: compared with the others above
+        const Span g = span(grads[i], i);
+        const Span *past = std::lower_bound(w.get(), w.get() + n, g.last,
+                                            [](const Span &a, uintptr_t end) { return a.first < end; });
+        if (past != w.get() && past[-1].last > g.first) return overlap(i, past[-1].i);
+    }
+    return CSP_OK;
+}
+
 csp_status run_clip(const void *const *grads, void *const *outs, const int64_t *numel, const int32_t *dtypes,
                     int64_t count, float max_norm, float *norm, void *work, int64_t work_bytes, bool clip,
                     hipStream_t s)
@@ -282,6 +320,10 @@ csp_status run_clip(const void *const *grads, void *const *outs, const int64_t *
             return set_error(CSP_ERR_INVALID_ARG, "tensor %lld: NULL or misaligned pointer", (long long)i);
         chunks += chunks_of(grads[i], numel[i], esz);
         bytes += numel[i] * esz;
+    }
+    if (clip) {
+        const csp_status st = outputs_apart(grads, outs, numel, dtypes, count);
+        if (st != CSP_OK) return st;
     }
     Entry *table = (Entry *)work;
     double *partial = (double *)((char *)work + p.partial_off);

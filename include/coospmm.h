@@ -449,7 +449,8 @@ csp_status grad_norm(const void *const *grads, const int64_t *numel, const int32
 /*
  * grad_clip -- that norm, and outs[i] = grads[i] * min(1, max_norm / (norm +
  * 1e-6)).  outs[i] is grads[i] (in place) or a tensor of the same size and
- * type that overlaps none of the others.  A NaN norm makes every output NaN.
+ * type that overlaps none of the others; overlapping tensors, one listed twice
+ * among them, are refused.  A NaN norm makes every output NaN.
  * max_norm >= 0.
  */
 csp_status grad_clip(const void *const *grads, void *const *outs, const int64_t *numel, const int32_t *dtypes,

@@ -1,0 +1,40 @@
+"""What the token operators refuse beyond a single bad argument: tensors that overlap.  Nothing here reaches the GPU:
+every call returns before a launch."""
+import ctypes
+import os
+
+import pytest
+
+from coo_spmm_fwd_amd import binding as csp
+
+P = ctypes.c_void_p(4096)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(csp.LIB_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
+    return csp.load()
+
+
+def test_grad_clip_refuses_tensors_that_overlap(lib):
+    """One workgroup would read what another has scaled: the result would depend on which came first."""
+    need = lib.grad_clip_workspace(3)
+    dt = (ctypes.c_int32 * 3)(0, 0, 1)
+    n = (ctypes.c_int64 * 3)(100, 50, 10)
+    ptr = lambda *a: (ctypes.c_void_p * 3)(*a)
+
+    def clip(g, o, n=n):
+        return lib.grad_clip(g, o, n, dt, 3, ctypes.c_float(1.0), P, P, need, None)
+
+    apart = ptr(4096, 8192, 12288)
+    for g in (ptr(4096, 4096, 12288),      # one tensor listed twice, in place
+              ptr(4096, 4492, 12288),      # one that begins in the last element of another
+              ptr(12288, 8192, 12270)):    # in any order
+        assert clip(g, g) == -1 and "overlap" in csp.sparse_layer_last_error()
+    for o in (ptr(20480, 20480, 28672),    # outputs on each other
+              ptr(8192, 20480, 28672),     # an output on another tensor's gradient
+              ptr(4100, 20480, 28672),     # an output beside its own gradient's start
+              ptr(20480, 24576, 24596)):
+        assert clip(apart, o) == -1 and "overlap" in csp.sparse_layer_last_error()

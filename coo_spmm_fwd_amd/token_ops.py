@@ -92,6 +92,8 @@ def linear_cross_entropy(X, W, targets):
 
 @torch.no_grad()
 def clip_grad_norm(params, max_norm: float):
-    """Scale the parameters' gradients in place by min(1, max_norm / (norm + 1e-6)); returns the norm
-    over all of them before that, as an fp32 tensor [1].  A parameter listed twice is an error."""
+    """Scale the gradients of the parameters (or of the one parameter) in place by min(1, max_norm / (norm +
+    1e-6)); returns the norm over all of them before that, as an fp32 tensor [1].  A parameter listed twice
+    is an error."""
+    params = [params] if isinstance(params, torch.Tensor) else params
     return csp.grad_clip([p.grad for p in params if p.grad is not None], max_norm)

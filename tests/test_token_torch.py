@@ -79,3 +79,28 @@ def test_second_gradients_pass_through_the_embedding(plain):
         if f is ops.embedding:
             mine = second
     assert torch.allclose(mine, second)
+
+
+@pytest.fixture
+def clipped(monkeypatch):
+    """The lists of gradients that clip_grad_norm hands to the library."""
+    lists = []
+
+    def grad_clip(grads, max_norm):
+        lists.append(list(grads))
+        for g in grads:
+            g.numpy()[...] *= 0.5  # as the library does: torch does not see the write
+        return torch.ones(1)
+
+    monkeypatch.setattr(ops.csp, "grad_clip", grad_clip)
+    return lists
+
+
+def test_clipping_takes_one_tensor_too(clipped):
+    p = torch.nn.Parameter(torch.ones(3, 2))
+    p.grad = torch.ones(3, 2)
+    ops.clip_grad_norm(p, 1.0)
+    assert [g is p.grad for g in clipped[0]] == [True]
+    q = torch.nn.Parameter(torch.ones(2))
+    ops.clip_grad_norm((r for r in (p, q)), 1.0)  # and any iterable; q has no gradient
+    assert [g is p.grad for g in clipped[1]] == [True]

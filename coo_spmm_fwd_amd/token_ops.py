@@ -96,4 +96,7 @@ def clip_grad_norm(params, max_norm: float):
     1e-6)); returns the norm over all of them before that, as an fp32 tensor [1].  A parameter listed twice
     is an error."""
     params = [params] if isinstance(params, torch.Tensor) else params
-    return csp.grad_clip([p.grad for p in params if p.grad is not None], max_norm)
+    grads = [p.grad for p in params if p.grad is not None]
+    norm = csp.grad_clip(grads, max_norm)
+    torch.autograd.graph.increment_version(grads)  # a write in place that torch did not see
+    return norm

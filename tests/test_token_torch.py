@@ -104,3 +104,14 @@ def test_clipping_takes_one_tensor_too(clipped):
     q = torch.nn.Parameter(torch.ones(2))
     ops.clip_grad_norm((r for r in (p, q)), 1.0)  # and any iterable; q has no gradient
     assert [g is p.grad for g in clipped[1]] == [True]
+
+
+def test_clipping_counts_as_a_write(clipped):
+    """A graph that saved a gradient before it was clipped refuses to use it, as after any write in place."""
+    p = torch.nn.Parameter(torch.ones(3, 2))
+    (g,) = torch.autograd.grad(p.pow(3).sum(), p, create_graph=True)
+    loss = g.square().sum()  # saves g
+    p.grad = g.detach()
+    ops.clip_grad_norm([p], 1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()

@@ -27,6 +27,11 @@ __device__ __forceinline__ float2 loss_of(float mx, float s, float z)
     return z == INFINITY ? make_float2(NAN, NAN) : make_float2((float)(fmax(rest, (double)z) + l), (float)(fmax(d, 0.0) + l));
 }
 
+// P at a token's target, p - 1, from p and the sum of its others.  p alone is off by half a step of lse, 10^-6
+// beside logits of 20, and the gradient of a smaller loss, 1 - p, would be lost.  All of exp(z - lse) are off by
+// the same factor, which the quotient takes out.
+__device__ __forceinline__ float target_of(float p, float others) { return -others / (others + p); }
+
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 

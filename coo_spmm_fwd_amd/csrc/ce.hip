@@ -14,7 +14,8 @@
 // tokens cost nothing.  The logits are not stored: the forward keeps a
 // maximum and a sum for each (vocabulary tile, token); the backward recomputes
 // the logits, a piece of the vocabulary at a time, from the saved lse, and
-// keeps P = exp(z - lse) - [v = t] of that piece only.  (A small vocabulary
+// keeps P = exp(z - lse) - [v = t] of that piece only; P at the target takes the
+// sum of the others (target_of in ce.h).  (A small vocabulary
 // times few tokens makes too few tiles for 256 CUs: there the width is cut,
 // and the parts' logits, a few MiB in the workspace, are read once more.)
 //
@@ -426,6 +427,16 @@ __global__ __launch_bounds__(kCeThreads) void k_ce_loss(Parts z, const int32_t *
     loss[rows[n]] = r.y;
 }
 
+// An element of P into its planes.
+template <bool kMany>
+__device__ __forceinline__ void put_p(uint16_t *p, int64_t plane, float x)
+{
+    uint32_t b[kPPlanes<kMany>];
+    split_pair(x, 0.0f, b);
+#pragma unroll
+    for (int pl = 0; pl < kPPlanes<kMany>; ++pl) p[pl * plane] = (uint16_t)b[pl];
+}
+
 // P of row blockIdx.x (planes), zeros for columns past the vocabulary and for tokens past the list, up to the
 // next multiple of 64 (the depth of dW).
 template <bool kMany>
@@ -439,13 +450,21 @@ __global__ __launch_bounds__(kCeThreads) void k_ce_p(Parts z, const int32_t *__r
     const bool on = n < cnt;
     const float ls = on ? lse[rows[n]] * kLog2e : 0.0f;
     const int64_t t = on ? tgt[n] : -1;
+    __shared__ float sum[kCeThreads / 64], pt;
+    float others = 0.0f;
     for (int64_t v = threadIdx.x * 4; v < ldp; v += kCeThreads * 4) {
         float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (on && v < V) {
             const f32x4 y = logits_at(z, n, v);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (v + r < V) x[r] = exp_less(y[r], ls) - (v + r == t ? 1.0f : 0.0f);
+            for (int r = 0; r < 4; ++r) {
+                if (v + r < V) x[r] = exp_less(y[r], ls);
+                if (v + r == t) {
+                    pt = x[r];
+                    x[r] = 0.0f;
+                }
+                others += x[r];
+            }
         }
         uint32_t b[2][kPPlanes<kMany>];
 #pragma unroll
@@ -454,16 +473,27 @@ __global__ __launch_bounds__(kCeThreads) void k_ce_p(Parts z, const int32_t *__r
         for (int pl = 0; pl < kPPlanes<kMany>; ++pl)
             *(uint2 *)(P + pl * planep + n * ldp + v) = make_uint2(b[0][pl], b[1][pl]);
     }
+    if (!on) return;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) others += __shfl_xor(others, off, 64);
+    if ((threadIdx.x & 63) == 0) sum[threadIdx.x >> 6] = others;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < kCeThreads / 64; ++w) others += sum[w];
+    put_p<kMany>(P + n * ldp + t, planep, target_of(pt, others));
 }
 
-// P of the piece (planes): P[n][v], zeros for tokens past the list and columns past the piece, so
-// that it can serve as depth up to the next multiple of 64.
+// P of the piece (planes) without the targets' elements: P[n][v], zeros for tokens past the list and columns
+// past the piece, so that it can serve as depth up to the next multiple of 64.  For k_ce_targets: the sum of the
+// elements of each wave row of the vocabulary tiles and token, and exp(z - lse) at the target.
 template <int BN, bool kMany>
 __global__ __launch_bounds__(kTileThreads, 2) void k_ce_probs(Logits a,
                                                                                 const float *__restrict__ lse,
                                                                                 const int32_t *__restrict__ rows,
                                                                                 uint16_t *__restrict__ P, int64_t ldp,
-                                                                                int64_t planep)
+                                                                                int64_t planep,
+                                                                                float *__restrict__ others,
+                                                                                float *__restrict__ pt)
 {
     using T = Tile<false, false, kBM, BN, kWavesM<BN>, kWavesN<BN>>;
     using S = Stage<16 * T::FM, 16, uint16_t>;
@@ -487,6 +517,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_probs(Logits a,
         const bool target = __ballot(t >= 0) != 0;  // few waves hold one
         const float ls = on ? lse[rows[n]] * kLog2e : 0.0f;
         const int end = on ? valid : 0;
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
             float x[4];
@@ -494,10 +525,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_probs(Logits a,
             for (int r = 0; r < 4; ++r) x[r] = exp_less(tile.acc[i][j][r], ls);
             if (target)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] -= t == 16 * i + r ? 1.0f : 0.0f;
+                for (int r = 0; r < 4; ++r)
+                    if (t == 16 * i + r) {
+                        pt[n] = x[r];
+                        x[r] = 0.0f;
+                    }
             if (edge)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[r] = 16 * i + r < end ? x[r] : 0.0f;
+            sum += (x[0] + x[1]) + (x[2] + x[3]);
             uint32_t b[2][kOut];
 #pragma unroll
             for (int h = 0; h < 2; ++h) split_pair(x[2 * h], x[2 * h + 1], b[h]);
@@ -510,8 +546,42 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_probs(Logits a,
 #pragma unroll
         for (int pl = 0; pl < kOut; ++pl)
             S::store(mine + pl * S::kBytes, P + pl * planep + (nw + j * 16) * ldp + vw, ldp, 16, 16 * T::FM);
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+        if (g == 0 && on) others[((a.v0 / kBM + at.m) * kWavesM<BN> + wm) * a.npad + n] = sum;
         wait_lds();
     }
+}
+
+// The targets' elements of the piece [v0, v0 + nv), from the sum of each token's others over all `parts` of the
+// vocabulary.  16 threads a token, each over every 16th part.
+template <bool kMany>
+__global__ __launch_bounds__(1024) void k_ce_targets(const float *__restrict__ others, int64_t npad, int64_t parts,
+                                                     const float *__restrict__ pt,
+                                                     const int32_t *__restrict__ tgt, const int32_t *__restrict__ count,
+                                                     int64_t v0, int64_t nv, uint16_t *__restrict__ P, int64_t ldp,
+                                                     int64_t planep)
+{
+    constexpr int kAhead = 8;
+    __shared__ float join[16][64];
+    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t m = (int64_t)blockIdx.x * 64 + l, cnt = count[0];
+    if ((int64_t)blockIdx.x * 64 >= cnt) return;
+    float s = 0.0f;
+    if (m < cnt)
+        for (int64_t t = w; t < parts; t += 16 * kAhead) {
+            float x[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) x[j] = t + 16 * j < parts ? others[(t + 16 * j) * npad + m] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) s += x[j];
+        }
+    join[w][l] = s;
+    __syncthreads();
+    if (w != 0 || m >= cnt) return;
+    for (int i = 1; i < 16; ++i) s += join[i][l];
+    const int64_t t = tgt[m] - v0;
+    if (t >= 0 && t < nv) put_p<kMany>(P + m * ldp + t, planep, target_of(pt[m], s));
 }
 
 // acc[split][n][c] (+)= sum over the split's part of the piece of P[n, v] W[v, c].
@@ -622,8 +692,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typenam
 }
 
 // Memory of a call is bounded whatever the vocabulary: pieces of it are taken so that P stays within
-// kPieceBytes, and the planes (or the padded copy) of W within kCopyBytes.
-constexpr int64_t kPieceBytes = (int64_t)512 << 20;
+// kPieceBytes (or 256 vocabulary rows of all tokens, if that is more), and the planes (or the padded copy) of W
+// within kCopyBytes.  The backward of several pieces makes the logits of all of them first, for the sums that the
+// targets' elements are made of, and once more: so a piece is large.
+constexpr int64_t kPieceBytes = (int64_t)4 << 30;
 constexpr int64_t kCopyBytesF32 = (int64_t)1 << 30, kCopyBytesBF16 = (int64_t)256 << 20;
 
 // Tiles of logits up to which their depth is cut (step, whole / cut: 51 tiles, 2056 tokens x 707 x 1472, fp32 363 /
@@ -635,7 +707,7 @@ struct CePlan {
     int64_t npad, ldx, piece, tiles, splits, dw_splits, z_splits;
     int bn;
     bool copy;  // W is copied, a piece at a time: planes, or rows that are no multiple of 128 bytes
-    size_t rows, tgt, slot, count, X, W, part, zt, P, acc, dw_acc, z, total;
+    size_t rows, tgt, slot, count, X, W, part, zt, P, others, pt, acc, dw_acc, z, total;
 };
 
 // Into how many parts the depth of a product of `tiles` tiles is cut, so that its rounds of 256 (one tile a CU)
@@ -700,6 +772,8 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         p.zt = take(4 * p.npad);
     } else {
         p.P = take(p_planes * 2 * p.npad * p.piece);
+        p.others = take(4 * p.npad * p.tiles * kWavesM<128>);
+        p.pt = take(4 * p.npad);
         p.splits = cuts(ceil_div(D, kBM) * ceil_div(p.npad, p.bn), ceil_div(p.piece, least), 4 * p.npad * p.ldx);
         p.dw_splits = cuts(ceil_div(D, kBM) * ceil_div(p.piece, 256), ceil_div(N, least), 4 * p.piece * p.ldx);
         if (p.dw_splits > 1) p.dw_acc = take(4 * p.dw_splits * p.piece * p.ldx);
@@ -823,22 +897,42 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
     const int64_t planep = p.npad * p.piece;
     csp_status st = ce_begin<E>(p, X, targets, N, V, D, nullptr, nullptr, w, s);
     if (st != CSP_OK) return st;
+    float *others = (float *)(w + p.others), *pt = (float *)(w + p.pt);
+    auto probs = [&](const Logits &a) {
+        const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
+        if (p.bn == 128) k_ce_probs<128, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep, others, pt);
+        else k_ce_probs<256, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep, others, pt);
+        CSP_LAUNCHED("k_ce_probs");
+        return CSP_OK;
+    };
+    for (int64_t v0 = 0; N > 0 && V > p.piece && v0 < V; v0 += p.piece) {  // the sums of all pieces
+        Logits a;
+        st = ce_piece<E>(p, W, V, D, v0, w, &a, s);
+        if (st != CSP_OK) return st;
+        st = probs(a);
+        if (st != CSP_OK) return st;
+    }
     const int64_t per = round_up(ceil_div(p.piece, p.splits), kDepth);
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         Logits a;
         st = ce_piece<E>(p, W, V, D, v0, w, &a, s);
         if (st != CSP_OK) return st;
         if (N > 0) {
-            const unsigned grid = (unsigned)(ceil_div(a.nv, kBM) * ceil_div(N, p.bn));
             if (p.z_splits > 1) {
                 Parts z;
                 st = ce_logits<kMany>(p, a, N, w, &z, s);
                 if (st != CSP_OK) return st;
                 k_ce_p<kMany><<<(unsigned)round_up(N, kDepth), kCeThreads, 0, s>>>(z, rows, a.tgt, count, V, lse, P,
                                                                                    p.piece, planep);
-            } else if (p.bn == 128) k_ce_probs<128, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
-            else k_ce_probs<256, kMany><<<grid, kTileThreads, 0, s>>>(a, lse, rows, P, p.piece, planep);
-            CSP_LAUNCHED("k_ce_probs or k_ce_p");
+                CSP_LAUNCHED("k_ce_p");
+            } else {
+                st = probs(a);
+                if (st != CSP_OK) return st;
+                k_ce_targets<kMany><<<(unsigned)ceil_div(N, 64), 1024, 0, s>>>(
+                    others, p.npad, p.tiles * (p.bn == 128 ? kWavesM<128> : kWavesM<256>), pt, a.tgt, count, v0, a.nv,
+                    P, p.piece, planep);
+                CSP_LAUNCHED("k_ce_targets");
+            }
             const InputGrad d{P, a.W, p.piece, a.ldw, planep, a.planew, count, a.nv, D, p.splits, per,
                               (float *)(w + p.acc), p.ldx, p.npad * p.ldx, v0 > 0};
             const unsigned gx = (unsigned)(ceil_div(D, kBM) * ceil_div(N, p.bn) * p.splits);

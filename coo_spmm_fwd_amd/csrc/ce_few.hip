@@ -11,6 +11,7 @@
 //   forward   k_few_prep, k_few_rows (logits -> maximum and sum of each 128
 //             vocabulary rows), k_few_join
 //   backward  k_few_prep, k_few_rows (logits -> P -> dW rows, and P for dX),
+//             k_few_targets (the targets' elements of P and their rows of dW),
 //             k_few_dx, k_ce_out
 //
 // Measured: one token, W 50257 x 768 fp32 (154 MB): rows 34 us, the call 48 of
@@ -235,6 +236,8 @@ struct FewArgs {
     // backward
     const float *lse, *dmean, *total;
     u32x4 *Pf;     // [vocabulary / 32][block][plane]: rows 16 tokens, depth 32 vocabulary rows 8 q + j
+    float *others; // [token][workgroup]: sum of P besides the target
+    float *pt;     // exp(z - lse) at the target
 };
 
 template <typename E, int NB, bool kBackward, bool kStream>
@@ -411,8 +414,9 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
             a.part[(int64_t)blockIdx.x * (16 * NB) + tid] = make_float2(mx, s);
         }
     } else {
-        // P, and its planes: pf[b][pair] with tokens as depth
+        // P without the targets' elements (k_few_targets), its sums, and its planes: pf[b][pair] with tokens as depth
         PFrag<E> pf[2][Q];
+        float others[4 * NB] = {};
         uint16_t *mine = (uint16_t *)(lds + w * kPWave);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -423,8 +427,14 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
                 for (int j = 0; j < 8; ++j) {
                     const int t = 2 * u + (j >> 2), n = 16 * t + 4 * q + (j & 3);
                     x[j] = 0.0f;
-                    if (t < NB && n < count && v[b] < V)
-                        x[j] = exp_of(acc[b][t < NB ? t : 0][j & 3] - a.lse[a.rows[n]]) - (v[b] == a.tgt[n] ? 1.0f : 0.0f);
+                    if (t < NB && n < count && v[b] < V) {
+                        x[j] = exp_of(acc[b][t < NB ? t : 0][j & 3] - a.lse[a.rows[n]]);
+                        if (v[b] == a.tgt[n]) {
+                            a.pt[n] = x[j];
+                            x[j] = 0.0f;
+                        }
+                        others[4 * (t < NB ? t : 0) + (j & 3)] += x[j];
+                    }
                 }
                 pf[b][u] = planes_of<PP>(x);
                 // the same with vocabulary rows as depth, for dX
@@ -440,7 +450,15 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
                     }
                 }
             }
+#pragma unroll
+        for (int i = 0; i < 4 * NB; ++i) {
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) others[i] += __shfl_xor(others[i], off, 64);
+            if ((l & 15) == 0) join[w][16 * (i >> 2) + 4 * q + (i & 3)].x = others[i];
+        }
         lds_barrier();
+        if (tid < 16 * NB)
+            a.others[(int64_t)tid * gridDim.x + blockIdx.x] = join[0][tid].x + join[1][tid].x + join[2][tid].x + join[3][tid].x;
         u32x4 *out = a.Pf + ((int64_t)blockIdx.x * kFewWaves + w) * kPWave + l;
 #pragma unroll
         for (int i = 0; i < NB * PP; ++i) out[i * 64] = lds[w * kPWave + i * 64 + l];
@@ -512,6 +530,70 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
             lds_barrier();
         }
     }
+}
+
+// The targets' elements of P, put into Pf, and the rows of dW that they are in, written anew: a token's
+// element takes the sum of all its others (target_of), which a workgroup of k_few_rows does not have.  One workgroup for 256 columns of the row of the first token of each target; it is bound by the
+// latency of its loads, tens of KiB of P and X from L2 (32 tokens, width 768 fp32: 6 us; 64, 4096 bf16: 12).
+template <typename E, int NB>
+__global__ __launch_bounds__(kFewThreads) void k_few_targets(FewArgs a, const typename E::T *__restrict__ X, int64_t tiles,
+                                                             typename E::T *__restrict__ dW)
+{
+    constexpr int PP = Form<E>::kPPlanes, kMost = 16 * NB, kAhead = 16;
+    __shared__ float p[kMost];
+    __shared__ int32_t from[kMost], tgt[kMost];
+    const int cnt = a.count[0], m = blockIdx.x % kMost, tid = threadIdx.x, l = tid & 63, w = tid >> 6;
+    const int64_t D = a.D, c0 = (int64_t)(blockIdx.x / kMost) * kFewThreads;
+    if (m >= cnt) return;
+    if (tid < kMost) {
+        from[tid] = a.rows[tid < cnt ? tid : m];
+        tgt[tid] = tid < cnt ? a.tgt[tid] : -1;
+    }
+    __syncthreads();
+    const int32_t v = tgt[m];
+    if (__syncthreads_or(tid < m && tgt[tid] == v)) return;
+    // P[k][v] of Pf: tokens k, plane pl
+    uint16_t *column = (uint16_t *)(a.Pf + (int64_t)(v >> 5) * (NB * PP * 64) + 16 * (v >> 3 & 3)) + (v & 7);
+    auto place = [&](int k, int pl) { return (((k >> 4) * PP + pl) * 64 + (k & 15)) * 8; };
+    if (tid < kMost && tgt[tid] != v) {
+        float s = 0.0f;
+        if (tid < cnt)
+#pragma unroll
+            for (int pl = PP - 1; pl >= 0; --pl) s += __uint_as_float((uint32_t)column[place(tid, pl)] << 16);
+        p[tid] = s;
+    }
+    for (int k = m + w; k < cnt; k += kFewWaves) {  // the same sum in each of the row's workgroups
+        if (tgt[k] != v) continue;
+        float s = 0.0f;
+        for (int64_t t = l; t < tiles; t += 64 * kAhead) {
+            float x[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) x[j] = t + 64 * j < tiles ? a.others[k * tiles + t + 64 * j] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) s += x[j];
+        }
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) s += __shfl_xor(s, off, 64);
+        if (l == 0) p[k] = target_of(a.pt[k], s);
+    }
+    __syncthreads();
+    if (c0 == 0 && tid < kMost && tgt[tid] == v) {
+        uint32_t planes[PP];
+        split_pair(p[tid], 0.0f, planes);
+#pragma unroll
+        for (int pl = 0; pl < PP; ++pl) column[place(tid, pl)] = (uint16_t)planes[pl];
+    }
+    const int64_t c = c0 + tid;
+    if (c >= D) return;
+    float s = 0.0f;
+    for (int k = 0; k < cnt; k += kAhead) {  // past the list: P 0 beside a row that takes part
+        float x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) x[j] = E::load(X, from[k + j] * D + c);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) s = fmaf(p[k + j], x[j], s);
+    }
+    dW[v * D + c] = E::from_f(s * grad_scale(a.dmean, a.total));
 }
 
 // Joins the workgroups' maxima and sums, and adds the losses up.  One workgroup.
@@ -697,7 +779,7 @@ __global__ __launch_bounds__(kFewThreads, NB >= 4 ? 1 : 2) void k_few_dx(FewDx a
 struct FewPlan {
     int nb, splits, per;
     int64_t steps, frags, tiles, lda;  // depth steps of 32 of Xf, fragments of Xt, workgroups of 128 rows
-    size_t rows, tgt, slot, count, Xf, Xt, part, zt, Pf, acc, total;
+    size_t rows, tgt, slot, count, Xf, Xt, part, zt, Pf, others, pt, acc, total;
 };
 
 FewPlan few_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward)
@@ -726,6 +808,8 @@ FewPlan few_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward)
         p.frags = round_up(D, kFewCols) / 16;
         p.Xt = take(p.frags * ((p.nb + 1) / 2) * planes * 1024);
         p.Pf = take(p.tiles * kFewWaves * p.nb * (dtype == CSP_F32 ? 3 : 2) * 1024);
+        p.others = take(p.tiles * 16 * p.nb * 4);
+        p.pt = take(4 * kFewMost);
         // about two workgroups a CU; a wave has at least one step of 32 rows
         int64_t s = round_up(ceil_div(512, groups), 8);
         if (s > 128) s = 128;
@@ -796,6 +880,8 @@ csp_status bwd_few(const void *X, const void *W, const int64_t *targets, int64_t
     a.dmean = dmean;
     a.total = total;
     a.Pf = (u32x4 *)(w + p.Pf);
+    a.others = (float *)(w + p.others);
+    a.pt = (float *)(w + p.pt);
     // A W past the memory-side cache (256 MB) is not there for k_few_dx anyway, and streaming it leaves the
     // cache to dW (64 tokens, 537 MB: 546 / 513 us a step plain / streamed, with P in one plane; 154 MB: 177 / 190).
     if (V * D * (int64_t)sizeof(T) > (int64_t)256 << 20)
@@ -804,6 +890,8 @@ csp_status bwd_few(const void *X, const void *W, const int64_t *targets, int64_t
         k_few_rows<E, NB, true, false><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
     CSP_LAUNCHED("k_few_rows");
     if (N == 0) return CSP_OK;
+    k_few_targets<E, NB><<<(unsigned)(16 * NB * ceil_div(D, kFewThreads)), kFewThreads, 0, s>>>(a, (const T *)X, p.tiles, (T *)dW);
+    CSP_LAUNCHED("k_few_targets");
     const FewDx d{a.Pf, V, D, p.splits, p.per, (float *)(w + p.acc), p.lda, 16 * NB * p.lda};
     k_few_dx<E, NB><<<(unsigned)(p.splits * ceil_div(D, kDxCols<E>)), kFewThreads, 0, s>>>(d, (const T *)W);
     CSP_LAUNCHED("k_few_dx");

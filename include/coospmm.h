@@ -429,7 +429,9 @@ csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, i
  * Rows of dX of tokens that take no part are 0 and such tokens add nothing to
  * dW.  dX and dW have the dtype of X and W.  exp(z - lse) - [v = t] enters the
  * products with bf16 operands as a sum of two bf16 numbers (off by 2^-16 of
- * itself at most), with fp32 operands as a sum of three.
+ * itself at most), with fp32 operands as a sum of three.  At the target it takes
+ * the sum of the others in place of lse, so that gradients of small losses keep
+ * their digits too.
  */
 csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
                          csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX, void *dW,

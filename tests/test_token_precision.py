@@ -66,3 +66,25 @@ def test_gradients_hold_the_digits_of_p(N, V, D, mask, dtype):
     gX, gW = gradients(X, W, t)
     within(gX, dX, eX, "dX")
     within(gW, dW, eW, "dW")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V,D", [(1, 700, 96), (40, 700, 96), (100, 700, 96), (200, 30000, 96), (300, 300, 96)])
+def test_gradients_of_small_losses_keep_their_digits(N, V, D, dtype):
+    """Losses down to 1e-7 beside logits of 25: the target's element of G is 1 - p = 1 - e^-loss, which p - 1
+    with p = exp(z - lse) has lost.  It is off by what the loss is off by: d loss = (1 - e^-loss) dd, with d
+    the others' log-sum less the target's logit."""
+    g = gen(38)
+    t = torch.randint(0, V, (N,), generator=g, device="cuda")
+    W = torch.randn(V, D, generator=g, device="cuda").to(dtype)
+    lift = torch.linspace(0.1, 0.3, N, device="cuda")[:, None] if N > 1 else torch.full((1, 1), 0.25, device="cuda")
+    X = (W.float()[t] * lift).to(dtype)
+
+    def error(ez, z, lse):
+        return torch.expm1(2 * ez.amax(1) + (V + 16) * U32 + 4 * U32 * (z.abs().amax(1) + lse.abs()))
+
+    dX, eX, dW, eW = gradient_reference(X, W, t, error)
+    gX, gW = gradients(X, W, t)
+    within(gX, dX, eX, "dX")
+    within(gW, dW, eW, "dW")

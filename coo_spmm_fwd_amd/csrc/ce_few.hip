@@ -342,7 +342,9 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
 #pragma unroll
                 for (int t = 0; t < NB; ++t) {
                     const f32x4 y = acc[b][t] - lost[b][t], n = sum[b][t] + y;
-                    lost[b][t] = (n - sum[b][t]) - y;
+                    const f32x4 off = (n - sum[b][t]) - y;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) lost[b][t][r] = fabsf(n[r]) < INFINITY ? off[r] : 0.0f;  // infinities stay
                     sum[b][t] = n;
                 }
         }

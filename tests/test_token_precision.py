@@ -88,3 +88,44 @@ def test_gradients_of_small_losses_keep_their_digits(N, V, D, dtype):
     gX, gW = gradients(X, W, t)
     within(gX, dX, eX, "dX")
     within(gW, dW, eW, "dW")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1, 16, 17, 32, 33, 64, 65, 130])
+def test_an_infinite_logit_counts_as_nothing(N):
+    """bf16 rows of W with -inf where X is positive: logits of -inf, whichever part of the width they are in."""
+    V, D = 1100, 700
+    X, W, t = ce_inputs(N, V, D, BF16, 40, "none")
+    X = X.abs() + 1.0
+    t = t // 8 * 8 + 1                                          # never one of the rows below
+    W = W / 16                                                  # sums of positive terms stay moderate
+    at = torch.arange(0, V, 8, device="cuda")
+    W[at, (at * 37) % D] = -math.inf
+    loss, lse, total = csp.linear_ce_fwd(X, W, t)
+    keep = torch.ones(V, dtype=torch.bool, device="cuda")
+    keep[at] = False
+    z = X.double() @ W[keep].double().T
+    want = torch.logsumexp(z, 1)
+    zt = (X.double() * W[t].double()).sum(1)
+    ez = (D + 8) * U32 * (X.double() @ W[keep].double().abs().T).amax(1)
+    tol = ez + (V + 16) * U32 + 4 * U32 * (z.abs().amax(1) + want.abs())
+    within(lse, want, tol, "lse")
+    within(loss, want - zt, tol + ez + U32 * (want - zt).abs(), "loss")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N", [1, 16, 17, 32])
+def test_logits_of_up_to_32_tokens_carry_their_lost_digits(N, dtype):
+    """z_0 = 2^14 and 31 terms of 3/8 of its step 2^-9, each in a part of the width of its own: added one by one
+    to 2^14 in fp32 they vanish, together they are 11.6 steps.  z_1 = 2^14 alone, so that loss = softplus(z_1 -
+    z_0) moves by at least (1 - p) of what is lost.  Off by half a step for each logit."""
+    D, small = 32 * 128, 3 * 2.0 ** -12
+    X = torch.ones(N, D, device="cuda", dtype=dtype)
+    W = torch.zeros(2, D, device="cuda", dtype=dtype)
+    W[:, 0] = 2.0 ** 14
+    W[0, 128::128] = small
+    t = torch.zeros(N, dtype=torch.int64, device="cuda")
+    loss, _, _ = csp.linear_ce_fwd(X, W, t)
+    want = torch.nn.functional.softplus(torch.full((N,), -31 * small, dtype=torch.float64, device="cuda"))
+    within(loss, want, torch.full_like(want, 2.0 ** -9 + 8 * U32), "loss")

@@ -61,10 +61,10 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[2])
     p[1] = pack_bf16(a - low_of(p[0]), b - high_of(p[0]));
 }
 
-// dmean / count, with the count that the forward divided by.
+// dmean / count, with the count that the forward divided by; 0 where no token takes part, whatever dmean is.
 __device__ __forceinline__ float grad_scale(const float *dmean, const float *total)
 {
-    return dmean[0] / fmaxf(total[1], 1.0f);
+    return total[1] > 0.0f ? dmean[0] / total[1] : 0.0f;
 }
 
 namespace {

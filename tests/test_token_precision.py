@@ -129,3 +129,15 @@ def test_logits_of_up_to_32_tokens_carry_their_lost_digits(N, dtype):
     loss, _, _ = csp.linear_ce_fwd(X, W, t)
     want = torch.nn.functional.softplus(torch.full((N,), -31 * small, dtype=torch.float64, device="cuda"))
     within(loss, want, torch.full_like(want, 2.0 ** -9 + 8 * U32), "loss")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N", [0, 5, 100, 300])
+def test_no_target_takes_part_whatever_dmean_is(N, dtype):
+    """No targets: zero gradients, also where the gradient of the mean is no finite number."""
+    X, W, t = ce_inputs(N, 90, 40, dtype, 41, "all")
+    _, lse, total = csp.linear_ce_fwd(X, W, t)
+    for dmean in (math.inf, math.nan):
+        dX, dW = csp.linear_ce_bwd(X, W, t, lse, torch.full((1,), dmean, device="cuda"), total)
+        assert not dX.any() and not dW.any()

@@ -139,8 +139,9 @@ __global__ __launch_bounds__(kEmbedThreads) void k_embed_fwd(const typename E::T
     if (!p.live || p.group >= N) return;
     const int64_t id = ids[p.group];
     float s[Vec<E>::kPer] = {};
-    if (id >= 0 && id < V) add_row<E>(table + id * D + p.col, D, s);
-    put_row<E, kStream>(Y + p.group * D + p.col, D, s, scale);
+    const bool part = id >= 0 && id < V;
+    if (part) add_row<E>(table + id * D + p.col, D, s);
+    put_row<E, kStream>(Y + p.group * D + p.col, D, s, part ? scale : 0.0f);  // zero whatever the scale is
 }
 
 // order[] and ptr[] for one range of kSortIds ids a workgroup.  Each workgroup reads all N ids (from
@@ -328,7 +329,7 @@ __global__ __launch_bounds__(kEmbedThreads, 8) void k_embed_rows(EmbedGrad a, co
         if (at1 - at0 <= kPart) {
             float s[kPer] = {};
             add_tokens<E>(dY, a.D, p.col, a.sp, a.order, at0, at1, s);
-            if (p.live) put_row<E, kStream>(dE + (first + r) * a.D + p.col, a.D, s, a.scale);
+            if (p.live) put_row<E, kStream>(dE + (first + r) * a.D + p.col, a.D, s, at1 > at0 ? a.scale : 0.0f);
         }
         at0 = at1;
     }

@@ -141,3 +141,16 @@ def test_no_target_takes_part_whatever_dmean_is(N, dtype):
     for dmean in (math.inf, math.nan):
         dX, dW = csp.linear_ce_bwd(X, W, t, lse, torch.full((1,), dmean, device="cuda"), total)
         assert not dX.any() and not dW.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [3, 40])
+def test_rows_that_no_id_names_are_zero_whatever_the_scale(D, dtype):
+    ids = torch.tensor([2, -1, 7, 2], device="cuda")
+    E = torch.ones(5, D, device="cuda", dtype=dtype)
+    for scale in (math.inf, math.nan):
+        Y = csp.embed_fwd(E, ids, scale)
+        assert not Y[[1, 2]].any() and not torch.isfinite(Y[[0, 3]]).any()
+        dE = csp.embed_bwd(torch.ones(4, D, device="cuda", dtype=dtype), ids, 5, scale)
+        assert not dE[[0, 1, 3, 4]].any() and not torch.isfinite(dE[2]).any()

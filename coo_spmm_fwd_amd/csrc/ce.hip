@@ -691,12 +691,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_ce_dw(WeightGrad a, typenam
     }
 }
 
-// Memory of a call is bounded whatever the vocabulary: pieces of it are taken so that P stays within
-// kPieceBytes (or 256 vocabulary rows of all tokens, if that is more), and the planes (or the padded copy) of W
-// within kCopyBytes.  The backward of several pieces makes the logits of all of them first, for the sums that the
+// Memory of a call: pieces of the vocabulary are taken so that P stays within kPieceBytes (or 256 vocabulary rows
+// of all tokens, if that is more), and the planes (or the padded copy) of W within kCopyBytes.  Sums of parts that
+// run side by side take 512 MiB at most for each of the logits, dX and dW (cuts).  Beside these a call has the rows
+// of X (planes), dX in fp32, and 8 bytes (the backward 16) a token and 256 vocabulary rows.  The backward of several pieces makes the logits of all of them first, for the sums that the
 // targets' elements are made of, and once more: so a piece is large.
 constexpr int64_t kPieceBytes = (int64_t)4 << 30;
 constexpr int64_t kCopyBytesF32 = (int64_t)1 << 30, kCopyBytesBF16 = (int64_t)256 << 20;
+
+// A launch has fewer than 2^32 threads, 512 a tile.
+constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 1;
 
 // Tiles of logits up to which their depth is cut (step, whole / cut: 51 tiles, 2056 tokens x 707 x 1472, fp32 363 /
 // 231 us, bf16 124 / 119; 4 tiles, 209 x 501 x 2241, 426 / 134 and 125 / 90; 48 tiles, 500 x 3000 x 300, fp32 147 /
@@ -754,6 +758,10 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
         if (r < kPad) r = kPad;
         if (r < p.piece) p.piece = r;
     };
+    // and each launch within kMaxTiles
+    auto tiles_within = [&](int64_t others) { limit(kMaxTiles / others * kBM, 1); };
+    tiles_within(ceil_div(N > 0 ? N : 1, p.bn));
+    if (backward) tiles_within(ceil_div(D, kBM));
     if (p.copy) limit(dtype == CSP_F32 ? kCopyBytesF32 : kCopyBytesBF16, planes * 2 * p.ldx);
     if (backward) limit(kPieceBytes, p_planes * 2 * p.npad);
     // an fp32 step of depth is six: its parts may be shorter
@@ -792,8 +800,10 @@ size_t ce_bytes(int64_t N, int64_t V, int64_t D, int dtype, bool backward)
 
 csp_status ce_args(int64_t N, int64_t V, int64_t D, int dtype)
 {
-    // a launch has fewer than 2^32 threads (256 a token, 2 a vocabulary row); 32-bit offsets in a tile
-    if (N < 0 || N >= (int64_t)1 << 24 || V < 1 || V > (int64_t)1 << 30 || D < 1 || D >= (int64_t)1 << 22)
+    // A launch has fewer than 2^32 threads: 256 a token (of a multiple of 64), 2 a vocabulary row, 512 a tile of dX
+    // (those of the logits and dW are cut with the vocabulary, ce_plan); 32-bit offsets in a tile.
+    if (N < 0 || N > ((int64_t)1 << 24) - kDepth || V < 1 || V > (int64_t)1 << 30 || D < 1 || D >= (int64_t)1 << 22 ||
+        ceil_div(N, 256) * ceil_div(D, kBM) > kMaxTiles)
         return set_error(CSP_ERR_INVALID_ARG, "bad shape: %lld tokens, vocabulary %lld, width %lld", (long long)N,
                          (long long)V, (long long)D);
     if (dtype != CSP_F32 && dtype != CSP_BF16) return set_error(CSP_ERR_DTYPE, "unsupported dtype %d", dtype);

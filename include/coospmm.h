@@ -379,13 +379,15 @@ csp_status sparse_layer_time_next(sparse_layer_t layer, void *ev_before, void *e
  * steps to the surrounding model).  They need no layer.  Token ids and targets
  * are int64 device arrays; an id or target outside [0, V) takes no part.
  * dtype is the type of the named matrices; sums are fp32, and each output is
- * rounded once (what else linear_ce rounds stands there).  A call that needs scratch memory takes a device workspace of
- * the caller (16-byte aligned, at least the bytes its _workspace function
- * says, contents undefined before and after).  All are asynchronous on
+ * rounded once (what else linear_ce rounds stands there).  A call that needs
+ * scratch memory takes a device workspace of the caller (16-byte aligned, at
+ * least the bytes its _workspace function says, contents undefined before and
+ * after).  All are asynchronous on
  * "stream", allocate nothing and may be captured in a HIP graph.  No float
  * result depends on the order of atomics: the same inputs give the same bits.
- * Limits: N, V, D < 2^31 (linear_ce: N < 2^24, V <= 2^30, D < 2^22); N = 0 is valid.  The _workspace functions return -1
- * for arguments that the call would refuse.
+ * Limits: N, V, D < 2^31; linear_ce: N <= 2^24 - 64, V <= 2^30, D < 2^22 and
+ * N D < 2^39; N = 0 is valid.  The _workspace functions return -1 for arguments
+ * that the call would refuse.
  */
 
 /*

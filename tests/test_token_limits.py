@@ -38,3 +38,13 @@ def test_grad_clip_refuses_tensors_that_overlap(lib):
               ptr(4100, 20480, 28672),     # an output beside its own gradient's start
               ptr(20480, 24576, 24596)):
         assert clip(apart, o) == -1 and "overlap" in csp.sparse_layer_last_error()
+
+
+def test_linear_ce_refuses_what_no_launch_could_hold(lib):
+    """A launch has fewer than 2^32 threads: 256 a token, 512 a tile of 256 x 256 of dX."""
+    for dt in (0, 1):
+        for backward in (0, 1):
+            size = lambda N, V, D: lib.linear_ce_workspace(N, V, D, dt, backward)
+            assert size(2**24 - 64, 100, 8) > 0 and size(2**24 - 63, 100, 8) == -1
+            assert size(2**22, 100, 2**16) > 0 and size(2**22, 100, 2**18) == -1
+    assert lib.linear_ce_fwd(P, P, P, 2**24 - 63, 100, 8, 1, P, P, P, P, 2**60, None) == -1

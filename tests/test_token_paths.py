@@ -94,3 +94,20 @@ def test_linear_ce_in_pieces(dtype, N, V, D, how):
     X, W, t = ce_inputs(N, V, D, dtype, 8, "some")
     t[0], t[1] = V - 1, 0
     ce_check(X, W, t)
+
+
+@pytest.mark.gpu
+def test_more_tiles_than_a_launch_holds():
+    """2^21 tokens, few of which take part, and 300001 vocabulary rows: 9.6 million tiles, 4.9e9 threads."""
+    N, V, D = 2**21 + 300, 300_001, 64
+    assert -(-N // 256) * -(-V // 256) * 512 > 2**32
+    W = (torch.randn(V, D, generator=gen(9), device="cuda") / 4).bfloat16()
+    X = torch.randn(N, D, generator=gen(10), device="cuda").bfloat16()
+    t = torch.full((N,), -100, device="cuda")
+    rows = torch.arange(5, N, 9973, device="cuda")
+    t[rows] = torch.randint(0, V, rows.shape, generator=gen(11), device="cuda")
+    t[rows[0]], t[rows[-1]] = V - 1, 0
+    loss, lse, total = csp.linear_ce_fwd(X, W, t)
+    one, oness, _ = csp.linear_ce_fwd(X[rows], W, t[rows])     # the same tokens alone
+    assert torch.equal(loss[rows], one) and torch.equal(lse[rows], oness)
+    assert float(total[1]) == rows.numel() and not loss[t < 0].any()

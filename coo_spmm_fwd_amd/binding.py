@@ -25,7 +25,7 @@ EXPORTED = ["sparse_layer_create", "sparse_layer_destroy", "spmm_fwd", "spmm_fwd
             "sparse_layer_export_index", "sparse_layer_values", "sparse_layer_set_values", "sparse_layer_time_next",
             "sparse_layer_last_error", "restructure_async", "sparse_layer_sync", "spmm_batch_minor", "spmm_fwd_bm",
             "spmm_bwd_bm", "embed_fwd", "embed_bwd", "embed_bwd_workspace", "linear_ce_fwd", "linear_ce_bwd",
-            "linear_ce_workspace", "grad_norm", "grad_clip", "grad_clip_workspace"]
+            "linear_ce_bwd_input", "linear_ce_bwd_weight", "linear_ce_workspace", "grad_norm", "grad_clip", "grad_clip_workspace"]
 
 
 class CspError(RuntimeError):
@@ -112,6 +112,10 @@ def load(path: str = LIB_PATH):
     L.linear_ce_bwd.restype = c_int
     L.linear_ce_bwd.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p,
                                 c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]
+    for f in (L.linear_ce_bwd_input, L.linear_ce_bwd_weight):
+        f.restype = c_int
+        f.argtypes = [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_void_p, c_void_p, c_void_p,
+                      c_void_p, c_void_p, c_int64, c_void_p]
     L.linear_ce_workspace.restype = c_int64
     L.linear_ce_workspace.argtypes = [c_int64, c_int64, c_int64, c_int, c_int32]
     L.grad_norm.restype = c_int
@@ -594,18 +598,40 @@ def linear_ce_fwd(X, W, targets, loss=None, lse=None, total=None, stream=None):
     return loss, lse, total
 
 
-def linear_ce_bwd(X, W, targets, lse, dmean, total, dX=None, dW=None, stream=None):
-    """Gradients (dX, dW) of dmean * mean loss; lse and total from linear_ce_fwd, dmean fp32 [1]."""
+def _ce_grad_inputs(X, W, targets, lse, dmean, total, stream):
+    """The library, a workspace, the arguments that all gradient calls begin with, and device and sizes."""
     here, xp, wp, tp, N, V, D, dt = _ce_inputs(X, W, targets)
-    L, dev, f32 = load(), X.device, _torch().float32
+    L, f32 = load(), _torch().float32
     ep = _ptr(lse, "lse", here, f32, (N,))
     gp, sp = _ptr(dmean, "dmean", here, f32, (1,)), _ptr(total, "total", here, f32, (3,))
-    w = _work(L.linear_ce_workspace(N, V, D, dt, 1), dev, stream)
+    w = _work(L.linear_ce_workspace(N, V, D, dt, 1), X.device, stream)
+    return L, w, (xp, wp, tp, N, V, D, dt, ep, gp, sp), (here, N, V, D)
+
+
+def linear_ce_bwd(X, W, targets, lse, dmean, total, dX=None, dW=None, stream=None):
+    """Gradients (dX, dW) of dmean * mean loss; lse and total from linear_ce_fwd, dmean fp32 [1]."""
+    L, w, args, (here, N, V, D) = _ce_grad_inputs(X, W, targets, lse, dmean, total, stream)
+    dev = X.device
     dX = _out(dX, "dX", here, X.dtype, (N, D), dev, stream)
     dW = _out(dW, "dW", here, X.dtype, (V, D), dev, stream)
-    _check(L.linear_ce_bwd(xp, wp, tp, N, V, D, dt, ep, gp, sp, dX.data_ptr(), dW.data_ptr(), w.data_ptr(), w.numel(),
-                           _stream(stream)))
+    _check(L.linear_ce_bwd(*args, dX.data_ptr(), dW.data_ptr(), w.data_ptr(), w.numel(), _stream(stream)))
     return dX, dW
+
+
+def linear_ce_bwd_input(X, W, targets, lse, dmean, total, dX=None, stream=None):
+    """dX of linear_ce_bwd alone, where W takes no gradient."""
+    L, w, args, (here, N, V, D) = _ce_grad_inputs(X, W, targets, lse, dmean, total, stream)
+    dX = _out(dX, "dX", here, X.dtype, (N, D), X.device, stream)
+    _check(L.linear_ce_bwd_input(*args, dX.data_ptr(), w.data_ptr(), w.numel(), _stream(stream)))
+    return dX
+
+
+def linear_ce_bwd_weight(X, W, targets, lse, dmean, total, dW=None, stream=None):
+    """dW of linear_ce_bwd alone, where X takes no gradient."""
+    L, w, args, (here, N, V, D) = _ce_grad_inputs(X, W, targets, lse, dmean, total, stream)
+    dW = _out(dW, "dW", here, X.dtype, (V, D), X.device, stream)
+    _check(L.linear_ce_bwd_weight(*args, dW.data_ptr(), w.data_ptr(), w.numel(), _stream(stream)))
+    return dW
 
 
 def _tensor_list(ts, name, like=None):

@@ -125,6 +125,7 @@ inline bool ce_is_few(int64_t N, int dtype) { return N <= (dtype == CSP_F32 ? 12
 size_t ce_few_bytes(int64_t N, int64_t V, int64_t D, int dtype, bool backward);
 csp_status ce_few_fwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D, int dtype,
                       float *loss, float *lse, float *total, char *work, hipStream_t s);
+// dX or dW may be NULL: not asked for.
 csp_status ce_few_bwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D, int dtype,
                       const float *lse, const float *dmean, const float *total, void *dX, void *dW, char *work,
                       hipStream_t s);

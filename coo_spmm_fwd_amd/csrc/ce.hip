@@ -812,6 +812,8 @@ csp_status ce_args(int64_t N, int64_t V, int64_t D, int dtype)
 
 bool aligned(const void *p, size_t a) { return p && (uintptr_t)p % a == 0; }
 
+enum Asked { kInput = 1, kWeight = 2 };
+
 // What both directions begin with: the list, the gathered rows of X, and the Logits arguments of a piece.
 template <typename E>
 csp_status ce_begin(const CePlan &p, const void *X, const int64_t *targets, int64_t N, int64_t V, int64_t D,
@@ -943,6 +945,8 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
                     P, p.piece, planep);
                 CSP_LAUNCHED("k_ce_targets");
             }
+        }
+        if (N > 0 && dX) {
             const InputGrad d{P, a.W, p.piece, a.ldw, planep, a.planew, count, a.nv, D, p.splits, per,
                               (float *)(w + p.acc), p.ldx, p.npad * p.ldx, v0 > 0};
             const unsigned gx = (unsigned)(ceil_div(D, kBM) * ceil_div(N, p.bn) * p.splits);
@@ -950,6 +954,7 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
             else k_ce_dx<256, kMany><<<gx, kTileThreads, 0, s>>>(d);
             CSP_LAUNCHED("k_ce_dx");
         }
+        if (!dW) continue;
         const WeightGrad g{P, a.X, p.piece, p.ldx, planep, a.planex, count, a.nv, D, dmean, total, p.dw_splits,
                            round_up(ceil_div(p.npad, p.dw_splits), kDepth), (float *)(w + p.dw_acc), p.ldx,
                            p.piece * p.ldx};
@@ -965,12 +970,31 @@ csp_status bwd_impl(const void *X, const void *W, const int64_t *targets, int64_
             CSP_LAUNCHED("k_ce_out");
         }
     }
-    if (N > 0) {
+    if (N > 0 && dX) {
         k_ce_out<E><<<out_blocks(N, D), 256, 0, s>>>((const float *)(w + p.acc), p.ldx, p.npad * p.ldx, (int)p.splits,
                                                      (const int32_t *)(w + p.slot), N, D, dmean, total, (T *)dX);
         CSP_LAUNCHED("k_ce_out");
     }
     return CSP_OK;
+}
+
+csp_status ce_bwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D, int dtype,
+                  const float *lse, const float *dmean, const float *total, void *dX, void *dW, int asked,
+                  void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    csp_status st = ce_args(N, V, D, dtype);
+    if (st != CSP_OK) return st;
+    const size_t e = dtype == CSP_BF16 ? 2 : 4;
+    if (!aligned(W, e) || (asked & kWeight && !aligned(dW, e)) || !aligned(dmean, 4) || !aligned(total, 4) ||
+        (N > 0 && (!aligned(X, e) || !aligned(targets, 8) || !aligned(lse, 4) || (asked & kInput && !aligned(dX, e)))))
+        return set_error(CSP_ERR_INVALID_ARG, "NULL or misaligned pointer");
+    const size_t need = ce_bytes(N, V, D, dtype, true);
+    if (!aligned(workspace, 16) || workspace_bytes < (int64_t)need)
+        return set_error(CSP_ERR_INVALID_ARG, "workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
+    auto run = dtype == CSP_BF16 ? bwd_impl<BF16> : bwd_impl<F32>;
+    if (ce_is_few(N, dtype))
+        return ce_few_bwd(X, W, targets, N, V, D, dtype, lse, dmean, total, dX, dW, (char *)workspace, stream);
+    return run(X, W, targets, N, V, D, lse, dmean, total, dX, dW, (char *)workspace, stream);
 }
 
 }  // namespace
@@ -1009,21 +1033,24 @@ csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, i
                          csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX, void *dW,
                          void *workspace, int64_t workspace_bytes, void *stream)
 {
-    using namespace csp;
-    csp_status st = ce_args(N, V, D, dtype);
-    if (st != CSP_OK) return st;
-    const size_t e = dtype == CSP_BF16 ? 2 : 4;
-    if (!aligned(W, e) || !aligned(dW, e) || !aligned(dmean, 4) || !aligned(total, 4) ||
-        (N > 0 && (!aligned(X, e) || !aligned(targets, 8) || !aligned(lse, 4) || !aligned(dX, e))))
-        return set_error(CSP_ERR_INVALID_ARG, "NULL or misaligned pointer");
-    const size_t need = ce_bytes(N, V, D, dtype, true);
-    if (!aligned(workspace, 16) || workspace_bytes < (int64_t)need)
-        return set_error(CSP_ERR_INVALID_ARG, "workspace of %lld bytes, %zu needed", (long long)workspace_bytes, need);
-    if (ce_is_few(N, dtype))
-        return ce_few_bwd(X, W, targets, N, V, D, dtype, lse, dmean, total, dX, dW, (char *)workspace, (hipStream_t)stream);
-    if (dtype == CSP_BF16)
-        return bwd_impl<BF16>(X, W, targets, N, V, D, lse, dmean, total, dX, dW, (char *)workspace, (hipStream_t)stream);
-    return bwd_impl<F32>(X, W, targets, N, V, D, lse, dmean, total, dX, dW, (char *)workspace, (hipStream_t)stream);
+    return csp::ce_bwd(X, W, targets, N, V, D, dtype, lse, dmean, total, dX, dW, csp::kInput | csp::kWeight, workspace,
+                       workspace_bytes, (hipStream_t)stream);
+}
+
+csp_status linear_ce_bwd_input(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
+                               csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX,
+                               void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return csp::ce_bwd(X, W, targets, N, V, D, dtype, lse, dmean, total, dX, nullptr, csp::kInput, workspace,
+                       workspace_bytes, (hipStream_t)stream);
+}
+
+csp_status linear_ce_bwd_weight(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
+                                csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dW,
+                                void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return csp::ce_bwd(X, W, targets, N, V, D, dtype, lse, dmean, total, nullptr, dW, csp::kWeight, workspace,
+                       workspace_bytes, (hipStream_t)stream);
 }
 
 }  // extern "C"

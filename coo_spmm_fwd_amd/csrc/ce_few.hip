@@ -466,6 +466,7 @@ __global__ __launch_bounds__(kFewThreads, NB > 4 ? 1 : 2) void k_few_rows(FewArg
         for (int i = 0; i < NB * PP; ++i) out[i * 64] = lds[w * kPWave + i * 64 + l];
         lds_barrier();
 
+        if (!dW) return;
         // dW[v][c] = scale * sum over tokens of X[n][c] P[n][v], 64 columns at a time
         const float scale = grad_scale(a.dmean, a.total);
         const int steps = (int)((D + kFewCols - 1) / kFewCols);
@@ -586,7 +587,7 @@ __global__ __launch_bounds__(kFewThreads) void k_few_targets(FewArgs a, const ty
         for (int pl = 0; pl < PP; ++pl) column[place(tid, pl)] = (uint16_t)planes[pl];
     }
     const int64_t c = c0 + tid;
-    if (c >= D) return;
+    if (c >= D || !dW) return;
     float s = 0.0f;
     for (int k = 0; k < cnt; k += kAhead) {  // past the list: P 0 beside a row that takes part
         float x[kAhead];
@@ -892,8 +893,10 @@ csp_status bwd_few(const void *X, const void *W, const int64_t *targets, int64_t
         k_few_rows<E, NB, true, false><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
     CSP_LAUNCHED("k_few_rows");
     if (N == 0) return CSP_OK;
-    k_few_targets<E, NB><<<(unsigned)(16 * NB * ceil_div(D, kFewThreads)), kFewThreads, 0, s>>>(a, (const T *)X, p.tiles, (T *)dW);
+    k_few_targets<E, NB><<<(unsigned)(16 * NB * (dW ? ceil_div(D, kFewThreads) : 1)), kFewThreads, 0, s>>>(
+        a, (const T *)X, p.tiles, (T *)dW);
     CSP_LAUNCHED("k_few_targets");
+    if (!dX) return CSP_OK;
     const FewDx d{a.Pf, V, D, p.splits, p.per, (float *)(w + p.acc), p.lda, 16 * NB * p.lda};
     k_few_dx<E, NB><<<(unsigned)(p.splits * ceil_div(D, kDxCols<E>)), kFewThreads, 0, s>>>(d, (const T *)W);
     CSP_LAUNCHED("k_few_dx");

@@ -59,7 +59,8 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dmean):
         X, W, targets, lse, total = ctx.saved_tensors
-        dX, dW = _LinearCrossEntropyGrad.apply(X, W, targets, lse, dmean.reshape(1).contiguous(), total)
+        need = ctx.needs_input_grad[:2]
+        dX, dW = _LinearCrossEntropyGrad.apply(X, W, targets, lse, dmean.reshape(1).contiguous(), total, need)
         return dX, dW, None
 
 
@@ -68,8 +69,11 @@ class _LinearCrossEntropyGrad(torch.autograd.Function):
     on a gradient, say) arrives here; otherwise they would pass for constants and their part be dropped."""
 
     @staticmethod
-    def forward(ctx, X, W, targets, lse, dmean, total):
-        return csp.linear_ce_bwd(X, W, targets, lse, dmean, total)
+    def forward(ctx, X, W, targets, lse, dmean, total, need):
+        args = X, W, targets, lse, dmean, total
+        if all(need):
+            return csp.linear_ce_bwd(*args)
+        return (csp.linear_ce_bwd_input(*args), None) if need[0] else (None, csp.linear_ce_bwd_weight(*args))
 
     @staticmethod
     def backward(ctx, *_):

@@ -438,7 +438,19 @@ csp_status linear_ce_fwd(const void *X, const void *W, const int64_t *targets, i
 csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
                          csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX, void *dW,
                          void *workspace, int64_t workspace_bytes, void *stream);
-/* backward: 0 for linear_ce_fwd, 1 for linear_ce_bwd. */
+
+/*
+ * linear_ce_bwd_input, linear_ce_bwd_weight -- one of the two gradients, where
+ * the other operand takes none (a frozen head, or hidden states that are
+ * inputs): the same bits, without the other's product, memory and traffic.
+ */
+csp_status linear_ce_bwd_input(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
+                               csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX,
+                               void *workspace, int64_t workspace_bytes, void *stream);
+csp_status linear_ce_bwd_weight(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
+                                csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dW,
+                                void *workspace, int64_t workspace_bytes, void *stream);
+/* backward: 0 for linear_ce_fwd, 1 for the gradients. */
 int64_t linear_ce_workspace(int64_t N, int64_t V, int64_t D, csp_dtype dtype, int32_t backward);
 
 /*

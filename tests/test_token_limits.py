@@ -48,3 +48,15 @@ def test_linear_ce_refuses_what_no_launch_could_hold(lib):
             assert size(2**24 - 64, 100, 8) > 0 and size(2**24 - 63, 100, 8) == -1
             assert size(2**22, 100, 2**16) > 0 and size(2**22, 100, 2**18) == -1
     assert lib.linear_ce_fwd(P, P, P, 2**24 - 63, 100, 8, 1, P, P, P, P, 2**60, None) == -1
+
+
+def test_one_gradient_alone_refuses_as_both_do(lib):
+    need = lib.linear_ce_workspace(4, 5, 8, 0, 1)
+    for f in (lib.linear_ce_bwd_input, lib.linear_ce_bwd_weight):
+        call = lambda X=P, W=P, t=P, N=4, V=5, D=8, dt=0, lse=P, dmean=P, total=P, out=P, w=P, nb=need: f(
+            X, W, t, N, V, D, dt, lse, dmean, total, out, w, nb, None)
+        for bad in ({"X": None}, {"W": None}, {"t": None}, {"lse": None}, {"dmean": None}, {"total": None}, {"out": None},
+                    {"w": None}, {"nb": need - 1}, {"N": -1}, {"V": 0}, {"D": 0}, {"out": ctypes.c_void_p(4098)},
+                    {"t": ctypes.c_void_p(4100)}, {"w": ctypes.c_void_p(4104)}):
+            assert call(**bad) == -1, bad
+        assert call(dt=3) == -6

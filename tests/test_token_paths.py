@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from coo_spmm_fwd_amd import binding as csp
+from coo_spmm_fwd_amd import token_ops as ops
 from tests.test_token_ops import BF16, F32, U32, ce_check, ce_inputs, gen, u, within
 
 
@@ -111,3 +112,31 @@ def test_more_tiles_than_a_launch_holds():
     one, oness, _ = csp.linear_ce_fwd(X[rows], W, t[rows])     # the same tokens alone
     assert torch.equal(loss[rows], one) and torch.equal(lse[rows], oness)
     assert float(total[1]) == rows.numel() and not loss[t < 0].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,V,D", [(0, 40, 24), (1, 500, 33), (40, 300, 100), (64, 1000, 64), (100, 700, 72),
+                                   (200, 300, 65), (300, 9000, 64), (700, 30_000, 128)])
+def test_one_gradient_alone_is_that_of_both(N, V, D, dtype):
+    X, W, t = ce_inputs(N, V, D, dtype, 12, "some")
+    _, lse, total = csp.linear_ce_fwd(X, W, t)
+    args = X, W, t, lse, torch.full((1,), 0.5, device="cuda"), total
+    dX, dW = csp.linear_ce_bwd(*args)
+    assert torch.equal(csp.linear_ce_bwd_input(*args), dX) and torch.equal(csp.linear_ce_bwd_weight(*args), dW)
+
+
+@pytest.mark.gpu
+def test_a_frozen_head_costs_no_gradient_of_it():
+    N, V, D = 48, 50_000, 512
+    X, W, t = ce_inputs(N, V, D, F32, 13, "none")
+    peak = {}
+    for frozen in (False, True):
+        x, w = X.clone().requires_grad_(), W.clone().requires_grad_(not frozen)
+        loss = ops.linear_cross_entropy(x, w, t)
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        loss.backward()
+        peak[frozen] = torch.cuda.max_memory_allocated() - before
+        assert (w.grad is None) == frozen and torch.isfinite(x.grad).all()
+    assert peak[False] - peak[True] > 0.9 * V * D * 4

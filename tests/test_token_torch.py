@@ -115,3 +115,23 @@ def test_clipping_counts_as_a_write(clipped):
     ops.clip_grad_norm([p], 1.0)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+@pytest.mark.parametrize("need", [(True, False), (False, True), (True, True)])
+def test_only_the_gradients_that_are_asked_for(plain, monkeypatch, need):
+    """A frozen head, or hidden states that are inputs: the other gradient is neither computed nor allocated."""
+    asked = []
+    for name, which in (("linear_ce_bwd", (True, True)), ("linear_ce_bwd_input", (True, False)),
+                        ("linear_ce_bwd_weight", (False, True))):
+        def call(*a, which=which):
+            asked.append(which)
+            got = plain_ce_bwd(*a)
+            return got if all(which) else got[which.index(True)]
+        monkeypatch.setattr(ops.csp, name, call, raising=False)
+    X, W, t = leaves()
+    both = torch.autograd.grad(ops.linear_cross_entropy(X, W, t), (X, W))
+    asked.clear()
+    X, W = X.detach().requires_grad_(need[0]), W.detach().requires_grad_(need[1])
+    ops.linear_cross_entropy(X, W, t).backward()
+    assert asked == [need]
+    assert all(p.grad is None if not n else torch.equal(p.grad, g) for p, n, g in zip((X, W), need, both))

@@ -40,7 +40,7 @@ constexpr int64_t kPart = 64;     // tokens a wave adds one after another
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortIds = 256;     // ids a workgroup of k_embed_sort looks for
-constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // a launch has fewer than 2^32 threads
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;  // a launch has fewer than 2^32 threads
 
 template <typename E> struct Vec;
 template <> struct Vec<F32> {
@@ -294,14 +294,14 @@ __device__ __forceinline__ bool slot_piece(const EmbedGrad &a, int64_t sl, int64
 
 template <typename E, bool kStream>
 __global__ __launch_bounds__(kEmbedThreads, 8) void k_embed_rows(EmbedGrad a, const typename E::T *__restrict__ dY,
-                                                              uint32_t piece_blocks, uint32_t every, int64_t slot0, int64_t v0,
+                                                              uint32_t piece_blocks, uint32_t every,
                                                               typename E::T *__restrict__ dE)
 {
     constexpr int kPer = Vec<E>::kPer;
     const uint32_t turn = blockIdx.x / every;  // of every `every` workgroups the first is a piece's
     if (turn < piece_blocks && turn * every == blockIdx.x) {
         const Lane p = lane_place(a.sp, turn, a.D, kPer);
-        const int64_t sl = slot0 + p.group;
+        const int64_t sl = p.group;
         int64_t id;
         int32_t from, to;
         if (sl >= 2 * ceil_div(a.N, kPart) || !slot_piece(a, sl, id, from, to)) return;
@@ -314,7 +314,7 @@ __global__ __launch_bounds__(kEmbedThreads, 8) void k_embed_rows(EmbedGrad a, co
         return;
     }
     const Lane p = lane_place(a.sp, blockIdx.x - (turn < piece_blocks ? turn + 1 : piece_blocks), a.D, kPer);
-    const int64_t first = v0 + (int64_t)p.group * kRowsPerLane;
+    const int64_t first = (int64_t)p.group * kRowsPerLane;
     // the rows' offsets: one load a lane, handed round
     const int lanes = 1 << a.sp.log2_lanes, l = threadIdx.x & 63, g0 = l & ~(lanes - 1);
     const int64_t left = a.V - first;
@@ -337,15 +337,14 @@ __global__ __launch_bounds__(kEmbedThreads, 8) void k_embed_rows(EmbedGrad a, co
 
 // One lane group for each cut in which an id of more than kPart tokens starts.
 template <typename E>
-__global__ __launch_bounds__(kEmbedThreads) void k_embed_join(EmbedGrad a, int64_t cut0,
-                                                              typename E::T *__restrict__ dE)
+__global__ __launch_bounds__(kEmbedThreads) void k_embed_join(EmbedGrad a, typename E::T *__restrict__ dE)
 {
     constexpr int kPer = Vec<E>::kPer;
     struct Row {
         float4 x[kPer / 4];
     };
     const Lane p = lane_place(a.sp, blockIdx.x, a.D, kPer);
-    const int64_t cut = cut0 + p.group;
+    const int64_t cut = p.group;
     int64_t id;
     int32_t from, to;
     if (cut >= ceil_div(a.N, kPart) || !slot_piece(a, 2 * cut + 1, id, from, to)) return;
@@ -421,18 +420,28 @@ csp_status embed_args(int64_t N, int64_t V, int64_t D, int dtype)
 
 bool aligned(const void *p, int dtype) { return p && (uintptr_t)p % (dtype == CSP_BF16 ? 2 : 4) == 0; }
 
-// f(first group, blocks) over `groups` lane groups (rows, or slots), as many a launch as its threads allow.
-template <typename F>
-csp_status by_groups(Strips sp, int64_t groups, F &&f)
+// Workgroups of `groups` lane groups (rows, or slots).
+int64_t blocks_of(Strips sp, int64_t groups) { return ceil_div(groups * sp.strips, kEmbedThreads >> sp.log2_lanes); }
+
+// Workgroups of the gradient's rows and pieces.  A workgroup of rows is 16 KiB of dE and more where there are many:
+// what one launch cannot hold, memory could not.
+struct GradBlocks {
+    int64_t cuts, rows, pieces;
+};
+GradBlocks grad_blocks(int64_t N, int64_t V, int64_t D, int dtype)
 {
-    const int64_t per_block = kEmbedThreads >> sp.log2_lanes;
-    int64_t most = kMaxBlocks * per_block / sp.strips;
-    if (most < 1) most = 1;  // strips are below 2^23: one row is at most 2^21 blocks
-    for (int64_t g = 0; g < groups; g += most) {
-        const int64_t n = groups - g < most ? groups - g : most;
-        const csp_status st = f(g, (unsigned)ceil_div(n * sp.strips, per_block));
-        if (st != CSP_OK) return st;
-    }
+    const Strips sp = strips_of(D, dtype == CSP_BF16 ? Vec<BF16>::kPer : Vec<F32>::kPer);
+    const int64_t cuts = N > kPart ? ceil_div(N, kPart) : 0;
+    return {cuts, blocks_of(sp, ceil_div(V, kRowsPerLane)), blocks_of(sp, 2 * cuts)};
+}
+csp_status embed_bwd_args(int64_t N, int64_t V, int64_t D, int dtype)
+{
+    const csp_status st = embed_args(N, V, D, dtype);
+    if (st != CSP_OK) return st;
+    const GradBlocks b = grad_blocks(N, V, D, dtype);
+    if (b.rows + b.pieces > kMaxBlocks)
+        return set_error(CSP_ERR_INVALID_ARG, "gradient of %lld x %lld and %lld tokens is too large for a launch",
+                         (long long)V, (long long)D, (long long)N);
     return CSP_OK;
 }
 
@@ -449,11 +458,13 @@ csp_status fwd_impl(const void *table, const int64_t *ids, int64_t N, int64_t V,
 {
     using T = typename E::T;
     const Strips sp = strips_of(D, Vec<E>::kPer);
-    return by_groups(sp, N, [&](int64_t n, unsigned blocks) {
-        k_embed_fwd<E, kStream><<<blocks, kEmbedThreads, 0, s>>>((const T *)table, V, D, ids + n, N - n, scale, sp, (T *)Y + n * D);
+    const int64_t most = kMaxBlocks * (kEmbedThreads >> sp.log2_lanes) / sp.strips;  // rows of a launch
+    for (int64_t n = 0; n < N; n += most) {
+        k_embed_fwd<E, kStream><<<(unsigned)blocks_of(sp, N - n < most ? N - n : most), kEmbedThreads, 0, s>>>(
+            (const T *)table, V, D, ids + n, N - n, scale, sp, (T *)Y + n * D);
         CSP_LAUNCHED("k_embed_fwd");
-        return CSP_OK;
-    });
+    }
+    return CSP_OK;
 }
 
 template <typename E, bool kStream>
@@ -482,31 +493,15 @@ csp_status bwd_impl(const void *dY, const int64_t *ids, int64_t N, int64_t V, in
     }
     const Strips sp = strips_of(D, Vec<E>::kPer);
     const EmbedGrad a{order, ptr, ids, D, V, N, sp, (float *)(w + p.part), p.ldp, scale};
-    const int64_t cuts = N > kPart ? ceil_div(N, kPart) : 0, rows = ceil_div(V, kRowsPerLane);
-    // pieces and rows share a launch where its threads suffice for both
-    const int64_t per_block = kEmbedThreads >> sp.log2_lanes;
-    const bool one = ceil_div(2 * cuts * sp.strips, per_block) + ceil_div(rows * sp.strips, per_block) <= kMaxBlocks;
-    const unsigned first = one ? (unsigned)ceil_div(2 * cuts * sp.strips, per_block) : 0;
-    if (!one) {
-        st = by_groups(sp, 2 * cuts, [&](int64_t slot, unsigned blocks) {
-            k_embed_rows<E, kStream><<<blocks, kEmbedThreads, 0, s>>>(a, (const T *)dY, blocks, 1, slot, 0, (T *)dE);
-            CSP_LAUNCHED("k_embed_rows");
-            return CSP_OK;
-        });
-        if (st != CSP_OK) return st;
-    }
-    st = by_groups(sp, rows, [&](int64_t g, unsigned blocks) {
-        const unsigned all = first + blocks, every = all >= 5 * first ? 5 : all >= 3 * first ? 3 : 1;  // odd: all XCDs
-        k_embed_rows<E, kStream><<<all, kEmbedThreads, 0, s>>>(a, (const T *)dY, first, every, 0, g * kRowsPerLane, (T *)dE);
-        CSP_LAUNCHED("k_embed_rows");
-        return CSP_OK;
-    });
-    if (st != CSP_OK) return st;
-    return by_groups(sp, cuts, [&](int64_t cut, unsigned blocks) {
-        k_embed_join<E><<<blocks, kEmbedThreads, 0, s>>>(a, cut, (T *)dE);
-        CSP_LAUNCHED("k_embed_join");
-        return CSP_OK;
-    });
+    const GradBlocks b = grad_blocks(N, V, D, sizeof(T) == 2 ? CSP_BF16 : CSP_F32);
+    const unsigned first = (unsigned)b.pieces, all = first + (unsigned)b.rows;
+    const unsigned every = all >= 5 * first ? 5 : all >= 3 * first ? 3 : 1;  // odd: all XCDs
+    k_embed_rows<E, kStream><<<all, kEmbedThreads, 0, s>>>(a, (const T *)dY, first, every, (T *)dE);
+    CSP_LAUNCHED("k_embed_rows");
+    if (b.cuts == 0) return CSP_OK;
+    k_embed_join<E><<<(unsigned)blocks_of(sp, b.cuts), kEmbedThreads, 0, s>>>(a, (T *)dE);
+    CSP_LAUNCHED("k_embed_join");
+    return CSP_OK;
 }
 
 }  // namespace
@@ -531,7 +526,7 @@ csp_status embed_fwd(const void *E, const int64_t *ids, int64_t N, int64_t V, in
 
 int64_t embed_bwd_workspace(int64_t N, int64_t V, int64_t D, csp_dtype dtype)
 {
-    if (csp::embed_args(N, V, D, dtype) != CSP_OK) return -1;
+    if (csp::embed_bwd_args(N, V, D, dtype) != CSP_OK) return -1;
     return (int64_t)csp::embed_plan(N, V, D).total;
 }
 
@@ -539,7 +534,7 @@ csp_status embed_bwd(const void *dY, const int64_t *ids, int64_t N, int64_t V, i
                      void *dE, void *workspace, int64_t workspace_bytes, void *stream)
 {
     using namespace csp;
-    csp_status st = embed_args(N, V, D, dtype);
+    csp_status st = embed_bwd_args(N, V, D, dtype);
     if (st != CSP_OK) return st;
     if (!aligned(dE, dtype) || (N > 0 && (!aligned(dY, dtype) || !ids || (uintptr_t)ids % 8)))
         return set_error(CSP_ERR_INVALID_ARG, "NULL or misaligned pointer");

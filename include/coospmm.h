@@ -385,8 +385,9 @@ csp_status sparse_layer_time_next(sparse_layer_t layer, void *ev_before, void *e
  * after).  All are asynchronous on
  * "stream", allocate nothing and may be captured in a HIP graph.  No float
  * result depends on the order of atomics: the same inputs give the same bits.
- * Limits: N, V, D < 2^31; linear_ce: N <= 2^24 - 64, V <= 2^30, D < 2^22 and
- * N D < 2^39; N = 0 is valid.  The _workspace functions return -1 for arguments
+ * Limits: N, V, D < 2^31 - 1; embed_bwd: a dE of less than about 275 GB;
+ * linear_ce: N <= 2^24 - 64, V <= 2^30, D < 2^22 and N D < 2^39; N = 0 is
+ * valid.  The _workspace functions return -1 for arguments
  * that the call would refuse.
  */
 

@@ -60,3 +60,11 @@ def test_one_gradient_alone_refuses_as_both_do(lib):
                     {"t": ctypes.c_void_p(4100)}, {"w": ctypes.c_void_p(4104)}):
             assert call(**bad) == -1, bad
         assert call(dt=3) == -6
+
+
+def test_lookup_gradient_refuses_what_no_launch_could_hold(lib):
+    """2^24 workgroups of 8 rows a lane group: dE of 280 GB."""
+    for dt, V, D in ((0, 2**31 - 2, 33), (1, 2**31 - 2, 68), (0, 2**20, 2**19)):
+        assert lib.embed_bwd_workspace(10, V, D, dt) == -1
+        assert lib.embed_bwd(P, P, 10, V, D, dt, 1.0, P, P, 2**60, None) == -1
+    assert lib.embed_bwd_workspace(10, 2**31 - 2, 16, 0) > 0 and lib.embed_bwd_workspace(10, 2**18, 2**18, 0) > 0

@@ -140,3 +140,16 @@ def test_a_frozen_head_costs_no_gradient_of_it():
         peak[frozen] = torch.cuda.max_memory_allocated() - before
         assert (w.grad is None) == frozen and torch.isfinite(x.grad).all()
     assert peak[False] - peak[True] > 0.9 * V * D * 4
+
+
+@pytest.mark.gpu
+def test_lookup_of_more_rows_than_a_launch_holds():
+    """4 rows of 33 vectors a workgroup: 2^26 rows and some are two launches (35 GB)."""
+    N, V, D = 2**26 + 1001, 5, 132
+    E = torch.randn(V, D, generator=gen(14), device="cuda")
+    ids = torch.arange(N, device="cuda") % (V + 1)              # the last is none
+    Y = csp.embed_fwd(E, ids, 2.0)
+    want = torch.cat([E * 2.0, torch.zeros(1, D, device="cuda")])
+    for n in range(0, N, 6 << 20):                              # a multiple of V + 1
+        part = Y[n:n + (6 << 20)]
+        assert torch.equal(part, want.repeat(-(-part.shape[0] // (V + 1)), 1)[:part.shape[0]]), n

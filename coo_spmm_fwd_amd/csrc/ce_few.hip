@@ -885,10 +885,13 @@ csp_status bwd_few(const void *X, const void *W, const int64_t *targets, int64_t
     a.Pf = (u32x4 *)(w + p.Pf);
     a.others = (float *)(w + p.others);
     a.pt = (float *)(w + p.pt);
-    // A W past the memory-side cache (256 MB) is not there for k_few_dx anyway, and streaming it leaves the
-    // cache to dW (64 tokens, 537 MB: 546 / 513 us a step plain / streamed, with P in one plane; 154 MB: 177 / 190).
-    if (V * D * (int64_t)sizeof(T) > (int64_t)256 << 20)
-        k_few_rows<E, NB, true, true><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
+    // A bf16 W past the memory-side cache (256 MB) is not there for k_few_dx anyway, and streaming it leaves the
+    // cache to dW (64 tokens, width 4096, step plain / streamed, us: 164 MB 251 / 256, 213 MB 282 / 283, 246 MB 308 /
+    // 300, 270 MB 433 / 412, 344 MB 456 / 434, 537 MB 581 / 559).  An fp32 W gains nothing (32 tokens, 154 MB 175 /
+    // 188, 281 MB 397 / 410, 412 MB 459 / 461; 128 tokens, 322 MB 764 / 765).
+    constexpr bool kMayStream = Form<E>::kPlanes == 1;
+    if (kMayStream && V * D * (int64_t)sizeof(T) > (int64_t)256 << 20)
+        k_few_rows<E, NB, true, kMayStream><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
     else
         k_few_rows<E, NB, true, false><<<(unsigned)p.tiles, kFewThreads, 0, s>>>(a, (const T *)W, (T *)dW);
     CSP_LAUNCHED("k_few_rows");

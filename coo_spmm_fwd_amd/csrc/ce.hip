@@ -33,14 +33,16 @@
 // into three bf16 planes (mfma_tile.h).
 //
 // Measured, 8192 tokens, 65536 x 4096 bf16 (4.4 TFLOP a product): forward
-// logits 3.43 ms (1280 TFLOP/s), backward logits 3.60 (1220), dX and dW 7 each for
-// two products; the library's plain product of that shape reaches 1485.  fp32 at
-// 2048 tokens, 30000 x 1024: 2.59 ms a step, 197 TFLOP/s of fp32 (1180 of bf16 products).
+// logits 3.40 ms (1290 TFLOP/s), backward logits 3.70 (1190), dX 7.02 and dW 6.75
+// for two products each (1250, 1300); the library's plain product of that shape
+// reaches 1485.  The matrix units are busy 68% of the forward's cycles and 61 to 62%
+// of the backward's, at 1.8 to 2.0 GHz.  fp32 at 2048 tokens, 30000 x 1024: 2.65 ms a step,
+// 190 TFLOP/s of fp32 (1140 of bf16 products).
 //
 // Up to 64 tokens (128 in fp32) go to ce_few.hip, where the products are bound by
-// the bytes of W: at 64 tokens bf16 this file took 763 us a step for its 513, at
-// 32 tokens fp32 573 for 175, at 65 fp32 (30000 x 1024) 490 for 274; at 65 bf16 it
-// takes 105.
+// the bytes of W.  A step here / there, us: 64 tokens bf16, 65536 x 4096 784 / 558 and
+// 30000 x 1024 129 / 114; 32 fp32, 50257 x 768 523 / 175; 30000 x 1024 fp32, 65 tokens 474 /
+// 284 and 128 tokens 475 / 296.  Past them, 30000 x 1024, 65 bf16 take 136, 129 fp32 502.
 #include "ce.h"
 #include "mfma_tile.h"
 
@@ -702,9 +704,9 @@ constexpr int64_t kCopyBytesF32 = (int64_t)1 << 30, kCopyBytesBF16 = (int64_t)25
 // A launch has fewer than 2^32 threads, 512 a tile.
 constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 1;
 
-// Tiles of logits up to which their depth is cut (step, whole / cut: 51 tiles, 2056 tokens x 707 x 1472, fp32 363 /
-// 231 us, bf16 124 / 119; 4 tiles, 209 x 501 x 2241, 426 / 134 and 125 / 90; 48 tiles, 500 x 3000 x 300, fp32 147 /
-// 133; but 88, 245 x 11095 x 192, 138 / 147 and 108, 300 x 9000 x 1024, 384 / 418).
+// Tiles of logits up to which their depth is cut (step, whole / cut: 51 tiles, 2056 tokens x 707 x 1472, fp32 374 /
+// 240 us, bf16 150 / 142; 4 tiles, 209 x 501 x 2241, 432 / 138 and 145 / 106; 48 tiles, 500 x 3000 x 300, 153 / 137 and
+// 115 / 115; but 88, 245 x 11095 x 192, 147 / 153 and 91 / 91, and 108, 300 x 9000 x 1024, 395 / 424 and 118 / 123).
 constexpr int64_t kFewTiles = 64;
 
 struct CePlan {
@@ -747,8 +749,8 @@ CePlan ce_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward, bool w
     p.npad = round_up(N > 0 ? N : 1, kPad);
     p.ldx = round_up(D, kDepth);
     // Tiles of 128 tokens for few of them, or where tiles of 256 would leave half of the CUs without work (step, tiles
-    // of 256 / 128: 256 tokens, 30000 x 1024, fp32 617 / 523 us, bf16 153 / 125; 384 tokens 735 / 791 and 174 / 172;
-    // 256 tokens, 65536 x 2048, 1942 / 2124 and 408 / 437).
+    // of 256 / 128: 256 tokens, 30000 x 1024, fp32 646 / 555 us, bf16 184 / 165; 300, 9000 x 1024, 494 / 393 and 149 /
+    // 118; 384, 30000 x 1024, 783 / 825 and 229 / 239; 256, 65536 x 2048, 2093 / 2260 and 545 / 583).
     p.bn = N <= 128 || ceil_div(V, kBM) * ceil_div(N, 256) <= 128 ? 128 : 256;
     p.copy = dtype == CSP_F32 || D % kDepth != 0 || !w_aligned;
     p.tiles = ceil_div(V, kBM);

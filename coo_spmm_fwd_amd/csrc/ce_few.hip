@@ -14,11 +14,11 @@
 //             k_few_targets (the targets' elements of P and their rows of dW),
 //             k_few_dx, k_ce_out
 //
-// Measured: one token, W 50257 x 768 fp32 (154 MB): rows 34 us, the call 48 of
-// which 14 are the two small kernels and the gaps.  One token, 65536 x 4096 bf16
+// Measured: one token, W 50257 x 768 fp32 (154 MB): rows 35 us, the call 47 of
+// which 12 are the two small kernels and the gaps.  One token, 65536 x 4096 bf16
 // (537 MB): 99 us a call, 5.4 TB/s.  64 tokens on that W: forward 118 us a call;
-// the training step 530 (2.15 GB, 4.1 TB/s; a 4 GiB copy moves 4.8).  32 tokens
-// on the fp32 W: rows 38, backward rows 73 (308 MB), dX 38, the step 178.
+// the training step 550 (2.15 GB, 3.9 TB/s; a 4 GiB copy moves 4.8).  32 tokens
+// on the fp32 W: rows 39, backward rows 74 (308 MB), dX 39, the step 188.
 //
 // A wave holds 32 vocabulary rows.  Its logits come out with a vocabulary row
 // a lane (lane % 16) and tokens 4 (lane / 16) + r in the registers, which is
@@ -96,7 +96,8 @@ __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c)
 // c += A B; of fp32 operands the six plane products above 2^-25 of the whole, small ones first.  P stands
 // beside bf16 operands in two planes, 16 bits: rounded to 8 it would add to a gradient of few terms, as those
 // of few tokens are, as much error again as the output's own rounding (one token: 0.0027 of the norm for 0.0016;
-// 64: 0.0019 for 0.0017), and it costs 7 us of 523 at 64 tokens.
+// 64: 0.0019 for 0.0017), and it costs 7 us of 523 at 64 tokens.  A third plane changed no digit of that error
+// (64 tokens: 15 us more).
 __device__ __forceinline__ f32x4 product(const Frag<BF16> &a, const Frag<BF16> &b, f32x4 c)
 {
     return mma(a.p[0], b.p[0], c);

@@ -1,5 +1,6 @@
-"""A small next-token model trained with the library alone: embedding, two truly sparse layers,
-cross entropy over the vocabulary, clipping, and a restructure of the sparse layers now and then.
+"""A small next-token model trained with the library's operators: embedding, two truly sparse layers,
+cross entropy over the vocabulary, clipping, and a restructure of the sparse layers now and then.  GELU,
+the residual sum and Adam are torch's.
 
     python -m coo_spmm_fwd_amd.token_lm [--steps 200] [--vocab 2000] [--width 256]
 
@@ -57,7 +58,7 @@ def text(n: int, vocab: int, seed: int):
 
 def train(steps: int = 200, vocab: int = 2000, width: int = 256, tokens: int = 512, lr: float = 0.02,
           restructure_every: int = 50, log=print):
-    """The losses of `steps` steps (read back once, at the end)."""
+    """The losses of `steps` steps (read back at the end; each line of the log reads one)."""
     model = TokenModel(vocab, width)
     params = list(model.parameters())
     opt = torch.optim.Adam(params, lr=lr)

@@ -382,13 +382,13 @@ csp_status sparse_layer_time_next(sparse_layer_t layer, void *ev_before, void *e
  * rounded once (what else linear_ce rounds stands there).  A call that needs
  * scratch memory takes a device workspace of the caller (16-byte aligned, at
  * least the bytes its _workspace function says, contents undefined before and
- * after).  All are asynchronous on
- * "stream", allocate nothing and may be captured in a HIP graph.  No float
- * result depends on the order of atomics: the same inputs give the same bits.
+ * after).  All are asynchronous on "stream", allocate nothing and may be
+ * captured in a HIP graph.  No float result depends on the order of atomics:
+ * the same inputs give the same bits.
  * Limits: N, V, D < 2^31 - 1; embed_bwd: a dE of less than about 275 GB;
  * linear_ce: N <= 2^24 - 64, V <= 2^30, D < 2^22 and N D < 2^39; N = 0 is
- * valid.  The _workspace functions return -1 for arguments
- * that the call would refuse.
+ * valid.  The _workspace functions return -1 for arguments that the call would
+ * refuse.
  */
 
 /*
@@ -443,7 +443,8 @@ csp_status linear_ce_bwd(const void *X, const void *W, const int64_t *targets, i
 /*
  * linear_ce_bwd_input, linear_ce_bwd_weight -- one of the two gradients, where
  * the other operand takes none (a frozen head, or hidden states that are
- * inputs): the same bits, without the other's product, memory and traffic.
+ * inputs): the same bits, without the other's product and traffic.  They take
+ * the workspace of linear_ce_bwd.
  */
 csp_status linear_ce_bwd_input(const void *X, const void *W, const int64_t *targets, int64_t N, int64_t V, int64_t D,
                                csp_dtype dtype, const float *lse, const float *dmean, const float *total, void *dX,

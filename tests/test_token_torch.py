@@ -135,3 +135,21 @@ def test_only_the_gradients_that_are_asked_for(plain, monkeypatch, need):
     ops.linear_cross_entropy(X, W, t).backward()
     assert asked == [need]
     assert all(p.grad is None if not n else torch.equal(p.grad, g) for p, n, g in zip((X, W), need, both))
+
+
+@pytest.mark.gpu
+def test_second_gradients_on_the_library():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    E, W = (torch.randn(9, 6, generator=g, device="cuda").requires_grad_() for _ in range(2))
+    ids, t = torch.tensor([3, -1, 3, 8], device="cuda"), torch.tensor([0, 5, -100, 8], device="cuda")
+    part = (ids >= 0)[:, None]
+    got = []
+    for look in (lambda: ops.embedding(ids, E, 2.0), lambda: torch.where(part, E[ids.clamp(min=0)] * 2.0, 0.0)):
+        y = look()
+        (first,) = torch.autograd.grad(y.pow(3).sum(), E, create_graph=True)
+        got.append(torch.autograd.grad(y.sum() + first.square().sum(), E)[0])
+    assert torch.allclose(*got, rtol=1e-5)
+    loss = ops.linear_cross_entropy(ops.embedding(ids, E, 2.0), W, t)
+    (first,) = torch.autograd.grad(loss, W, create_graph=True)
+    with pytest.raises(RuntimeError, match="cannot be differentiated"):
+        (loss + first.square().sum()).backward()
